@@ -28,8 +28,11 @@ __all__ = [
     "VR_RING_WEAK", "VR_PINGPONG_SAME_XCD", "VR_PINGPONG_WAVES", "VR_DISPATCH_NOALLOC_SCRATCH_BYTES",
     "VR_FENCE_NONE", "VR_FENCE_PUT", "VR_FENCE_GET",
     "VR_ASYNC_TIMEOUT", "VR_ASYNC_CAPACITY", "VR_ASYNC_BAD_EXPERT", "VR_ASYNC_LITMUS",
+    "VR_ASYNC_BAD_VALUE", "VR_ROUTE_RENORM", "VR_ACT_NONE", "VR_ACT_RELU", "VR_ACT_GELU", "VR_ACT_SILU", "VR_ACT_GATED",
+    "VR_MOE_LAYER_MAX_TOKENS",
     # argument structures and action helpers
     "vrCommRequirements", "vrRemoteAction", "vrLocalAction", "vrDevComm", "vrDevWindow",
+    "vrSlice", "vrLinearShape", "vrMoeShape",
     "SignalInc", "SignalAdd", "CounterInc", "VASignalInc", "VASignalAdd",
     # entry points
     "vr_error_string", "vr_version", "vr_comm_workspace_bytes", "vr_comm_create", "vr_comm_destroy",
@@ -42,6 +45,8 @@ __all__ = [
     "vr_allreduce", "vr_alltoall", "vr_alltoall_sessions", "vr_allgather",
     "vr_dispatch", "vr_dispatch_noalloc", "vr_dispatch_dedup", "vr_combine", "vr_combine_dedup",
     "vr_ring_exchange", "vr_signal_pingpong",
+    "vr_route", "vr_route_backward", "vr_linear_workspace_bytes", "vr_linear", "vr_linear_backward_workspace_bytes",
+    "vr_linear_backward", "vr_moe_layer_workspace_bytes", "vr_moe_layer",
 ]
 
 # The in-tree build; VRCOMM_LIB may name another build of the same library.
@@ -77,6 +82,10 @@ VR_PINGPONG_WAVES = 0x20
 VR_DISPATCH_NOALLOC_SCRATCH_BYTES = 4 << 20
 VR_FENCE_NONE, VR_FENCE_PUT, VR_FENCE_GET = 0x0, 0x1, 0x2
 VR_ASYNC_TIMEOUT, VR_ASYNC_CAPACITY, VR_ASYNC_BAD_EXPERT, VR_ASYNC_LITMUS = 0x1, 0x2, 0x4, 0x8
+VR_ASYNC_BAD_VALUE = 0x10
+VR_ROUTE_RENORM = 0x1
+VR_ACT_NONE, VR_ACT_RELU, VR_ACT_GELU, VR_ACT_SILU, VR_ACT_GATED = 0x0, 0x1, 0x2, 0x3, 0x10
+VR_MOE_LAYER_MAX_TOKENS = 64
 
 
 class VrError(RuntimeError):
@@ -113,6 +122,20 @@ class vrRemoteAction(Structure):
 
 class vrLocalAction(Structure):
     _fields_ = [("kind", c_uint32), ("id", c_uint32)]
+
+
+class vrSlice(Structure):
+    _fields_ = [("window", c_void_p), ("offset", c_uint64)]
+
+
+class vrLinearShape(Structure):
+    _fields_ = [("dtype", c_int), ("rows", c_int), ("groups", c_int), ("in_", c_int), ("out", c_int),
+                ("act", c_uint32)]
+
+
+class vrMoeShape(Structure):
+    _fields_ = [("dtype", c_int), ("tokens", c_int), ("hidden", c_int), ("inner", c_int), ("num_experts", c_int),
+                ("topk", c_int), ("act", c_uint32), ("flags", c_uint32)]
 
 
 def SignalInc(sig_id: int, strong: bool = True) -> vrRemoteAction:
@@ -186,6 +209,17 @@ SYMBOLS = {
     "vr_alltoall_sessions": (_R, [_P, _P, c_size_t, _P, c_size_t, c_size_t, c_uint32, c_uint32, c_uint32, _P]),
     "vr_va_signal_read": (_R, [_P, _P, c_int, c_size_t, c_int, POINTER(c_uint64)]),
     "vr_va_signal_reset": (_R, [_P, _P, c_int, c_size_t, _P]),
+    "vr_route": (_R, [_P, vrSlice, c_int, c_int, c_int, c_int, _P, _P, c_uint32, _P]),
+    "vr_route_backward": (_R, [_P, vrSlice, c_int, c_int, c_int, c_int, _P, _P, _P, vrSlice, c_uint32, _P]),
+    "vr_linear_workspace_bytes": (c_size_t, [c_int, POINTER(vrLinearShape)]),
+    "vr_linear": (_R, [_P, POINTER(vrLinearShape), vrSlice, vrSlice, vrSlice, vrSlice, _P, vrSlice, vrSlice, _P,
+                       c_size_t, _P]),
+    "vr_linear_backward_workspace_bytes": (c_size_t, [c_int, POINTER(vrLinearShape)]),
+    "vr_linear_backward": (_R, [_P, POINTER(vrLinearShape), vrSlice, vrSlice, vrSlice, vrSlice, _P, vrSlice, vrSlice,
+                                vrSlice, _P, c_size_t, _P]),
+    "vr_moe_layer_workspace_bytes": (c_size_t, [c_int, POINTER(vrMoeShape)]),
+    "vr_moe_layer": (_R, [_P, POINTER(vrMoeShape), vrSlice, _P, vrSlice, vrSlice, vrSlice, vrSlice, _P, _P, _P,
+                          c_size_t, _P]),
 }
 
 _lib = None
@@ -238,6 +272,15 @@ def _stream(stream) -> int:
 
 def _remote(a) -> vrRemoteAction:
     return vrRemoteAction(VR_ACTION_NONE, 0, 0, 0, 0) if a is None else a
+
+
+def _slice(s) -> vrSlice:
+    """A vrSlice, a (window, offset) pair, a window (offset 0), or None (absent)."""
+    if s is None:
+        return vrSlice(None, 0)
+    if isinstance(s, vrSlice):
+        return s
+    return vrSlice(*s) if isinstance(s, tuple) else vrSlice(s, 0)
 
 
 def _local(a) -> vrLocalAction:
@@ -467,3 +510,47 @@ def vr_ring_exchange(comm, send, recv, put_bytes, puts_per_rank, contexts, sig_b
     _check(lib().vr_ring_exchange(comm, send, recv, put_bytes, puts_per_rank, contexts, sig_base, cnt_base,
                                   sig_window, sig_window_off, _ptr(litmus) or None, flags, _stream(stream)),
            "vr_ring_exchange")
+
+
+def vr_route(comm, logits, dtype, T, K, num_experts, topk_idx, weights, flags=0, stream=None):
+    _check(lib().vr_route(comm, _slice(logits), dtype, T, K, num_experts, _ptr(topk_idx), _ptr(weights), flags,
+                          _stream(stream)), "vr_route")
+
+
+def vr_route_backward(comm, logits, dtype, T, K, num_experts, topk_idx, weights, dweights, dlogits, flags=0,
+                      stream=None):
+    _check(lib().vr_route_backward(comm, _slice(logits), dtype, T, K, num_experts, _ptr(topk_idx), _ptr(weights),
+                                   _ptr(dweights), _slice(dlogits), flags, _stream(stream)), "vr_route_backward")
+
+
+def vr_linear_workspace_bytes(nranks, shape) -> int:
+    return lib().vr_linear_workspace_bytes(nranks, ctypes.byref(shape))
+
+
+def vr_linear(comm, shape, x, w, out, bias=None, residual=None, preact=None, group_rows=None, workspace=None,
+              workspace_bytes=0, stream=None):
+    _check(lib().vr_linear(comm, ctypes.byref(shape), _slice(x), _slice(w), _slice(bias), _slice(residual),
+                           _ptr(group_rows), _slice(out), _slice(preact), _ptr(workspace), workspace_bytes,
+                           _stream(stream)), "vr_linear")
+
+
+def vr_linear_backward_workspace_bytes(nranks, shape) -> int:
+    return lib().vr_linear_backward_workspace_bytes(nranks, ctypes.byref(shape))
+
+
+def vr_linear_backward(comm, shape, dout, x, w, preact=None, dx=None, dw=None, dbias=None, group_rows=None,
+                       workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().vr_linear_backward(comm, ctypes.byref(shape), _slice(dout), _slice(x), _slice(w), _slice(preact),
+                                    _ptr(group_rows), _slice(dx), _slice(dw), _slice(dbias), _ptr(workspace),
+                                    workspace_bytes, _stream(stream)), "vr_linear_backward")
+
+
+def vr_moe_layer_workspace_bytes(nranks, shape) -> int:
+    return lib().vr_moe_layer_workspace_bytes(nranks, ctypes.byref(shape))
+
+
+def vr_moe_layer(comm, shape, x, router, w_up, w_down, out, topk_idx, weights, residual=None, workspace=None,
+                 workspace_bytes=0, stream=None):
+    _check(lib().vr_moe_layer(comm, ctypes.byref(shape), _slice(x), _ptr(router), _slice(w_up), _slice(w_down),
+                              _slice(residual), _slice(out), _ptr(topk_idx), _ptr(weights), _ptr(workspace),
+                              workspace_bytes, _stream(stream)), "vr_moe_layer")

@@ -1187,4 +1187,219 @@ vrResult_t vr_ring_exchange(vrComm_t c, vrWindow_t send, vrWindow_t recv, size_t
   return r;
 }
 
+// ---- the layers between the collectives ------------------------------------------------------
+// A required slice of n bytes per rank (elements of es bytes).
+static vrResult_t check_slice(vrComm* c, const vrSlice& s, size_t n, size_t es) {
+  if (!has_win(c, s.window)) return VR_ERR_INVALID_ARGUMENT;
+  if (s.offset % es || !span_ok(s.window, s.offset, n)) return VR_ERR_INVALID_ARGUMENT;
+  return va_touch(s.window, -1, s.offset, n) ? VR_ERR_INVALID_USAGE : VR_OK;
+}
+struct SliceUse {
+  const vrSlice* s;
+  size_t n;
+  bool written;
+};
+// Present slices are in their windows, and what is written overlaps nothing
+// else; `same` (if any) may be the very slice of `same_out`.
+static vrResult_t check_slices(vrComm* c, const SliceUse* use, int count, size_t es, const vrSlice* same,
+                               const vrSlice* same_out) {
+  for (int i = 0; i < count; ++i) {
+    if (!use[i].s->window) continue;
+    const vrResult_t r = check_slice(c, *use[i].s, use[i].n, es);
+    if (r != VR_OK) return r;
+  }
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < count; ++j) {
+      const vrSlice &a = *use[i].s, &b = *use[j].s;
+      if (i == j || !use[i].written || !a.window || !b.window) continue;
+      if (&a == same_out && &b == same && a.window == b.window && a.offset == b.offset) continue;
+      if (&a == same && &b == same_out && a.window == b.window && a.offset == b.offset) continue;
+      if (any_overlap(a.window, a.offset, use[i].n, b.window, b.offset, use[j].n, c->nranks))
+        return VR_ERR_INVALID_ARGUMENT;
+    }
+  return VR_OK;
+}
+static bool elem_ok(int dtype) { return dtype == VR_DT_F32 || dtype == VR_DT_BF16; }
+static bool workspace_ok(vrComm* c, const void* ws, size_t have, size_t need) {
+  if (!need) return true;
+  return ws && have >= need && reinterpret_cast<uintptr_t>(ws) % 256 == 0 && dev_span_ok(c, ws, need);
+}
+// Whether a device array lies clear of every rank's part of a slice.
+static bool clear_of(vrComm* c, const void* p, size_t n, const vrSlice& s, size_t sn) {
+  if (!p || !s.window) return true;
+  for (int r = 0; r < c->nranks; ++r)
+    if (overlap(static_cast<const char*>(p), n, s.window->base[r] + s.offset, sn)) return false;
+  return true;
+}
+
+static vrResult_t check_route(vrComm* c, int dtype, int T, int K, int E, uint32_t flags) {
+  if (!elem_ok(dtype) || (flags & ~VR_ROUTE_RENORM)) return VR_ERR_INVALID_ARGUMENT;
+  if (T < 0 || T >= 65536 || K < 1 || K > 64 || E < c->nranks || E % c->nranks || E > 1024)
+    return VR_ERR_INVALID_ARGUMENT;
+  return VR_OK;
+}
+
+vrResult_t vr_route(vrComm_t c, vrSlice logits, int dtype, int T, int K, int E, int32_t* topk, float* weights,
+                    uint32_t flags, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  vrResult_t r = check_route(c, dtype, T, K, E, flags);
+  if (r != VR_OK) return r;
+  const size_t es = dtype == VR_DT_F32 ? 4 : 2, n = es * T * E, m = (size_t)c->nranks * T * K * 4;
+  r = check_slice(c, logits, n, es);
+  if (r != VR_OK) return r;
+  if (!dev_span_ok(c, topk, m) || !dev_span_ok(c, weights, m)) return VR_ERR_INVALID_ARGUMENT;
+  if (overlap(reinterpret_cast<char*>(topk), m, reinterpret_cast<char*>(weights), m) ||
+      !clear_of(c, topk, m, logits, n) || !clear_of(c, weights, m, logits, n))
+    return VR_ERR_INVALID_ARGUMENT;
+  return launch_route(c, logits, dtype, T, K, E, topk, weights, (flags & VR_ROUTE_RENORM) != 0, S(stream));
+}
+
+vrResult_t vr_route_backward(vrComm_t c, vrSlice logits, int dtype, int T, int K, int E, const int32_t* topk,
+                             const float* weights, const float* dweights, vrSlice dlogits, uint32_t flags,
+                             void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  vrResult_t r = check_route(c, dtype, T, K, E, flags);
+  if (r != VR_OK) return r;
+  const bool renorm = (flags & VR_ROUTE_RENORM) != 0;
+  const size_t es = dtype == VR_DT_F32 ? 4 : 2, n = es * T * E, m = (size_t)c->nranks * T * K * 4;
+  if (!dlogits.window || (!renorm && !logits.window)) return VR_ERR_INVALID_ARGUMENT;
+  const SliceUse use[] = {{&logits, n, false}, {&dlogits, n, true}};
+  r = check_slices(c, use, 2, es, &logits, &dlogits);
+  if (r != VR_OK) return r;
+  if (!dev_span_ok(c, topk, m) || !dev_span_ok(c, weights, m) || !dev_span_ok(c, dweights, m))
+    return VR_ERR_INVALID_ARGUMENT;
+  if (!clear_of(c, topk, m, dlogits, n) || !clear_of(c, weights, m, dlogits, n) ||
+      !clear_of(c, dweights, m, dlogits, n))
+    return VR_ERR_INVALID_ARGUMENT;
+  return launch_route_backward(c, logits, dtype, T, K, E, topk, weights, dweights, dlogits, renorm, S(stream));
+}
+
+static bool act_ok(uint32_t act) { return !(act & ~(VR_ACT_GATED | 0x3u)); }
+static bool linear_ok(int R, const vrLinearShape* s) {
+  return R >= 1 && R <= VR_MAX_RANKS && s && elem_ok(s->dtype) && act_ok(s->act) && s->rows >= 0 &&
+         s->rows <= (1 << 24) && s->groups >= 1 && s->groups <= 1024 && s->in >= 1 && s->in <= (1 << 20) &&
+         s->out >= 1 && s->out <= (1 << 20);
+}
+size_t vr_linear_workspace_bytes(int nranks, const vrLinearShape* s) {
+  return linear_ok(nranks, s) ? linear_workspace_bytes(nranks, *s) : 0;
+}
+size_t vr_linear_backward_workspace_bytes(int nranks, const vrLinearShape* s) {
+  return linear_ok(nranks, s) ? linear_backward_workspace_bytes(nranks, *s) : 0;
+}
+
+// Bytes of a linear layer's tensors on one rank.
+struct LinearBytes {
+  size_t es, x, w, bias, out, z, counts;
+  LinearBytes(int R, const vrLinearShape& s) {
+    es = s.dtype == VR_DT_F32 ? 4 : 2;
+    const size_t n = (size_t)s.out * ((s.act & VR_ACT_GATED) ? 2 : 1);
+    x = es * s.rows * s.in;
+    w = es * s.groups * n * s.in;
+    bias = es * s.groups * n;
+    out = es * s.rows * s.out;
+    z = es * s.rows * n;
+    counts = sizeof(int32_t) * R * s.groups;
+  }
+};
+
+vrResult_t vr_linear(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w, vrSlice bias, vrSlice residual,
+                     const int32_t* group_rows, vrSlice out, vrSlice preact, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!linear_ok(c->nranks, s) || (!group_rows && s->groups > 1)) return VR_ERR_INVALID_ARGUMENT;
+  if (!x.window || !w.window || !out.window) return VR_ERR_INVALID_ARGUMENT;
+  const LinearBytes b(c->nranks, *s);
+  const SliceUse use[] = {{&x, b.x, false},         {&w, b.w, false},  {&bias, b.bias, false},
+                          {&residual, b.out, false}, {&out, b.out, true}, {&preact, b.z, true}};
+  vrResult_t r = check_slices(c, use, 6, b.es, &residual, &out);
+  if (r != VR_OK) return r;
+  if (group_rows && (!dev_span_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out) ||
+                     !clear_of(c, group_rows, b.counts, preact, b.z)))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t need = linear_workspace_bytes(c->nranks, *s);
+  if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
+  if (need)
+    for (const SliceUse& u : use)
+      if (!clear_of(c, ws, need, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
+  if (!s->rows) return VR_OK;
+  return launch_linear(c, *s, x, w, bias, residual, group_rows, out, preact, static_cast<char*>(ws), S(stream));
+}
+
+vrResult_t vr_linear_backward(vrComm_t c, const vrLinearShape* s, vrSlice dout, vrSlice x, vrSlice w, vrSlice preact,
+                              const int32_t* group_rows, vrSlice dx, vrSlice dw, vrSlice dbias, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!linear_ok(c->nranks, s) || (!group_rows && s->groups > 1)) return VR_ERR_INVALID_ARGUMENT;
+  if (!dout.window || (dw.window && !x.window) || (dx.window && !w.window) ||
+      (s->act != VR_ACT_NONE && !preact.window) || (!dx.window && !dw.window && !dbias.window))
+    return VR_ERR_INVALID_ARGUMENT;
+  const LinearBytes b(c->nranks, *s);
+  const SliceUse use[] = {{&dout, b.out, false}, {&x, b.x, false}, {&w, b.w, false},     {&preact, b.z, false},
+                          {&dx, b.x, true},      {&dw, b.w, true}, {&dbias, b.bias, true}};
+  vrResult_t r = check_slices(c, use, 7, b.es, nullptr, nullptr);
+  if (r != VR_OK) return r;
+  if (group_rows && !dev_span_ok(c, group_rows, b.counts)) return VR_ERR_INVALID_ARGUMENT;
+  const size_t need = linear_backward_workspace_bytes(c->nranks, *s);
+  if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
+  for (const SliceUse& u : use)
+    if (!clear_of(c, ws, need, *u.s, u.n) || (u.written && !clear_of(c, group_rows, b.counts, *u.s, u.n)))
+      return VR_ERR_INVALID_ARGUMENT;
+  return launch_linear_backward(c, *s, dout, x, w, preact, group_rows, dx, dw, dbias, static_cast<char*>(ws),
+                                S(stream));
+}
+
+static bool moe_ok(int R, const vrMoeShape* s) {
+  return R >= 1 && R <= VR_MAX_RANKS && s && elem_ok(s->dtype) && act_ok(s->act) && !(s->flags & ~VR_ROUTE_RENORM) &&
+         s->tokens >= 0 && (int64_t)R * s->tokens <= VR_MOE_LAYER_MAX_TOKENS && s->hidden >= 1 &&
+         s->hidden <= (1 << 20) && s->inner >= 1 && s->inner <= (1 << 20) && s->num_experts >= R &&
+         s->num_experts % R == 0 && s->num_experts <= 1024 && s->topk >= 1 && s->topk <= 64 &&
+         s->topk <= s->num_experts;
+}
+size_t vr_moe_layer_workspace_bytes(int nranks, const vrMoeShape* s) {
+  return moe_ok(nranks, s) ? moe_layer_workspace_bytes(nranks, *s) : 0;
+}
+
+vrResult_t vr_moe_layer(vrComm_t c, const vrMoeShape* s, vrSlice x, const void* router, vrSlice w_up, vrSlice w_down,
+                        vrSlice residual, vrSlice out, int32_t* topk, float* weights, void* ws, size_t ws_bytes,
+                        void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!moe_ok(c->nranks, s) || !x.window || !w_up.window || !w_down.window || !out.window)
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t es = s->dtype == VR_DT_F32 ? 4 : 2, per = s->num_experts / c->nranks;
+  const size_t row = es * s->tokens * s->hidden, mat = es * s->hidden * s->inner;
+  const size_t nr = es * s->num_experts * s->hidden, m = (size_t)c->nranks * s->tokens * s->topk * 4;
+  const SliceUse use[] = {{&x, row, false},
+                          {&w_up, per * mat * ((s->act & VR_ACT_GATED) ? 2 : 1), false},
+                          {&w_down, per * mat, false},
+                          {&residual, row, false},
+                          {&out, row, true}};
+  vrResult_t r = check_slices(c, use, 5, es, &residual, &out);
+  if (r != VR_OK) return r;
+  if (reinterpret_cast<uintptr_t>(router) % es || !dev_span_ok(c, router, nr) || !dev_span_ok(c, topk, m) ||
+      !dev_span_ok(c, weights, m))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t need = moe_layer_workspace_bytes(c->nranks, *s);
+  if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
+  const struct {
+    const void* p;
+    size_t n;
+    bool written;
+  } arr[] = {{router, nr, false}, {topk, m, true}, {weights, m, true}, {ws, need, true}};
+  for (int i = 0; i < 4; ++i) {
+    for (const SliceUse& u : use)
+      if ((u.written || arr[i].written) && !clear_of(c, arr[i].p, arr[i].n, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if ((arr[i].written || arr[j].written) &&
+          overlap(static_cast<const char*>(arr[i].p), arr[i].n, static_cast<const char*>(arr[j].p), arr[j].n))
+        return VR_ERR_INVALID_ARGUMENT;
+  }
+  return launch_moe_layer(c, *s, x, router, w_up, w_down, residual, out, topk, weights, static_cast<char*>(ws),
+                          S(stream));
+}
+
 }  // extern "C"

@@ -128,6 +128,32 @@ vrResult_t launch_alltoall_sessions(vrComm* c, const vrDevWindow& send, size_t s
                                     size_t recv_off, size_t block, uint32_t sig, const U64Tab& target, uint32_t index,
                                     uint64_t bar_base, hipStream_t st);
 
+vrResult_t launch_route(vrComm* c, const vrSlice& logits, int dtype, int T, int K, int E, int32_t* topk,
+                        float* weights, bool renorm, hipStream_t st);
+vrResult_t launch_route_backward(vrComm* c, const vrSlice& logits, int dtype, int T, int K, int E,
+                                 const int32_t* topk, const float* weights, const float* dweights,
+                                 const vrSlice& dlogits, bool renorm, hipStream_t st);
+size_t linear_workspace_bytes(int R, const vrLinearShape& s);
+size_t linear_backward_workspace_bytes(int R, const vrLinearShape& s);
+vrResult_t launch_linear(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrSlice& w, const vrSlice& bias,
+                         const vrSlice& residual, const int32_t* group_rows, const vrSlice& out,
+                         const vrSlice& preact, char* ws, hipStream_t st);
+vrResult_t launch_linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dout, const vrSlice& x,
+                                  const vrSlice& w, const vrSlice& preact, const int32_t* group_rows,
+                                  const vrSlice& dx, const vrSlice& dw, const vrSlice& dbias, char* ws,
+                                  hipStream_t st);
+size_t moe_layer_workspace_bytes(int R, const vrMoeShape& s);
+vrResult_t launch_moe_layer(vrComm* c, const vrMoeShape& s, const vrSlice& x, const void* router, const vrSlice& w_up,
+                            const vrSlice& w_down, const vrSlice& residual, const vrSlice& out, int32_t* topk,
+                            float* weights, char* ws, hipStream_t st);
+
+// The ranks' parts of a slice (nulls when it is absent).
+inline WinTab slice_tab(const vrSlice& s) {
+  WinTab t;
+  for (int r = 0; r < VR_MAX_RANKS; ++r) t.p[r] = s.window && s.window->base[r] ? s.window->base[r] + s.offset : nullptr;
+  return t;
+}
+
 // helpers in comm.hip
 vrResult_t ensure_scratch(vrComm* c, size_t bytes);
 vrResult_t launch_pingpong(vrComm* c, const vrWindow* w, size_t off, size_t bytes, uint32_t iters, uint32_t sig,

@@ -1,0 +1,223 @@
+// Shared by the layer kernels (route.hip, linear.hip, moe_layer.hip): element
+// traits, activations, wave reductions and the row ranges of groups.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "vr_device.hpp"
+#include "vr_internal.hpp"
+
+namespace vr {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef unsigned short v4h __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+// fp32 -> bf16 bits, round to nearest even (the hardware conversion; a NaN
+// stays one).
+__device__ inline uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
+__device__ inline uint32_t bf16_pack(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, v2bf{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+}
+
+template <int DT> struct Elem;
+template <> struct Elem<VR_DT_F32> {
+  typedef float T;
+  static constexpr int kSize = 4;
+  static constexpr int kChunk = 4;  // elements of 16 bytes
+  __device__ static float load(const void* p, uint64_t i) { return load4f_global(static_cast<const char*>(p) + 4 * i); }
+  __device__ static void store(void* p, uint64_t i, float f) { static_cast<float*>(p)[i] = f; }
+  __device__ static float round(float f) { return f; }
+};
+template <> struct Elem<VR_DT_BF16> {
+  typedef uint16_t T;
+  static constexpr int kSize = 2;
+  static constexpr int kChunk = 8;
+  __device__ static float load(const void* p, uint64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(load2_global(static_cast<const char*>(p) + 2 * i)) << 16);
+  }
+  __device__ static void store(void* p, uint64_t i, float f) { static_cast<uint16_t*>(p)[i] = bf16_bits(f); }
+  __device__ static float round(float f) { return __uint_as_float(static_cast<uint32_t>(bf16_bits(f)) << 16); }
+};
+
+// N consecutive elements (N * size at most 16 bytes); any element alignment:
+// the global loads and stores of this chip take it.
+template <int DT, int N> __device__ inline void load_n(const void* p, uint64_t i, float* f) {
+  const char* q = static_cast<const char*>(p) + i * Elem<DT>::kSize;
+  if constexpr (N == 1) {
+    f[0] = Elem<DT>::load(p, i);
+  } else {
+    typename Elem<DT>::T t[N];
+    __builtin_memcpy(t, __builtin_assume_aligned(q, Elem<DT>::kSize), sizeof(t));
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (DT == VR_DT_F32) f[j] = t[j];
+      else f[j] = __uint_as_float(static_cast<uint32_t>(t[j]) << 16);
+    }
+  }
+}
+template <int DT, int N> __device__ inline void store_n(void* p, uint64_t i, const float* f) {
+  char* q = static_cast<char*>(p) + i * Elem<DT>::kSize;
+  if constexpr (DT == VR_DT_F32) {
+    __builtin_memcpy(__builtin_assume_aligned(q, 4), f, 4 * N);
+  } else if constexpr (N == 1) {
+    Elem<DT>::store(p, i, f[0]);
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) w[j] = bf16_pack(f[2 * j], f[2 * j + 1]);
+    __builtin_memcpy(__builtin_assume_aligned(q, 2), w, 2 * N);
+  }
+}
+
+// ---- activations ------------------------------------------------------------------
+// y = act(z), in binary32: relu max(z, 0) (a NaN stays one); gelu
+// z (1 + erf(z / sqrt 2)) / 2; silu z / (1 + exp(-z)).
+__device__ inline float act_value(float z, uint32_t act) {
+  switch (act & 0xFu) {
+    case VR_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
+    case VR_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case VR_ACT_SILU: return z / (1.0f + expf(-z));
+    default: return z;
+  }
+}
+// act(z) and its derivative.
+__device__ inline void act_both(float z, uint32_t act, float* y, float* dy) {
+  switch (act & 0xFu) {
+    case VR_ACT_RELU:
+      *y = z > 0.0f || z != z ? z : 0.0f;
+      *dy = z > 0.0f ? 1.0f : 0.0f;
+      return;
+    case VR_ACT_GELU: {
+      const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+      *y = z * cdf;
+      *dy = cdf + z * expf(-0.5f * z * z) * 0.3989422804014327f;  // the normal density, 1 / sqrt(2 pi)
+      return;
+    }
+    case VR_ACT_SILU: {
+      const float s = 1.0f / (1.0f + expf(-z));
+      *y = z * s;
+      *dy = s * (1.0f + z * (1.0f - s));
+      return;
+    }
+    default:
+      *y = z;
+      *dy = 1.0f;
+  }
+}
+
+// ---- wave reductions (all 64 lanes; every lane gets the result) --------------------
+__device__ inline float wave_max(float v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// ---- groups -------------------------------------------------------------------------
+// A group's rows [first, first + count) of a rank, and its row tiles: the
+// groups' tiles are counted in order from 0, each group's rows rounded up to
+// whole tiles.
+struct GroupTile {
+  int g;      // -1: no such tile
+  int first;  // first row of the group
+  int count;  // its rows
+  int tile0;  // its first tile
+};
+
+// The group that holds tile `want` (BY_GROUP: group `want` itself), tiles of
+// bm rows. counts: the rank's [G] group_rows, or null (one group, all rows).
+// Every lane of the wave calls it with the same arguments. A negative count is
+// taken as 0, and rows past `rows` are left out; either sets
+// VR_ASYNC_CAPACITY (the caller that asks for 0 looks at every count).
+template <bool BY_GROUP>
+__device__ inline GroupTile find_group(const int32_t* counts, int G, int rows, int bm, int want, uint32_t* err) {
+  if (!counts) return {BY_GROUP || want < (rows + bm - 1) / bm ? 0 : -1, 0, rows, 0};
+  const int lane = static_cast<int>(lane_id());
+  int row0 = 0, tile0 = 0;
+  bool bad = false;
+  GroupTile t = {-1, 0, 0, 0};
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    const int c = g0 + lane < G ? counts[g0 + lane] : 0;
+    const int pos = max(c, 0);
+    int64_t s = pos;  // sums of 64 counts pass 32 bits
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int64_t o = __shfl_up(s, m);
+      if (lane >= m) s += o;
+    }
+    const int64_t end = s + row0;
+    const int lo = static_cast<int>(end - pos < rows ? end - pos : rows);
+    const int hi = static_cast<int>(end < rows ? end : rows);
+    bad |= c < 0 || end > rows;
+    const int n = (hi - lo + bm - 1) / bm;
+    int k = n;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int o = __shfl_up(k, m);
+      if (lane >= m) k += o;
+    }
+    const uint64_t here = BY_GROUP ? ballot(g0 + lane == want) : ballot(tile0 + k > want);
+    if (here && t.g < 0) {
+      const int src = __builtin_ctzll(here);
+      t.g = g0 + src;
+      t.first = __builtin_amdgcn_readlane(lo, src);
+      t.count = __builtin_amdgcn_readlane(hi, src) - t.first;
+      t.tile0 = tile0 + __builtin_amdgcn_readlane(k - n, src);
+      if (want) break;
+    }
+    row0 = __builtin_amdgcn_readlane(hi, 63);
+    tile0 += __builtin_amdgcn_readlane(k, 63);
+  }
+  if (ballot(bad) && lane == 0) atomic_or_u32(err, VR_ASYNC_CAPACITY);
+  return t;
+}
+
+// ---- 16-byte pieces of a row -----------------------------------------------------------
+// The piece's first n elements (n may be past either end of the piece), the
+// others 0. Any element alignment.
+template <int DT>
+__device__ inline v4u load_piece(const char* p, int n) {
+  v4u v = {0, 0, 0, 0};
+  if (n >= Elem<DT>::kChunk) {
+    __builtin_memcpy(&v, __builtin_assume_aligned(p, Elem<DT>::kSize), 16);
+  } else if (n > 0) {
+#pragma unroll
+    for (int j = 0; j < Elem<DT>::kChunk - 1; ++j) {
+      if constexpr (DT == VR_DT_F32) {
+        if (j < n) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
+      } else {
+        if (j < n) v[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
+      }
+    }
+  }
+  return v;
+}
+
+// ---- matrix instructions -----------------------------------------------------------------
+// acc[i][j] += sum_k a[i][k] b[j][k] over one 16-byte piece per lane: lane l
+// holds elements k = (l / 16) * piece ... of row i = l % 16 of a and j = l % 16
+// of b; of acc it holds i = (l / 16) * 4 + 0..3, j = l % 16. bf16: 32 k per
+// call, fp32: 16.
+template <int DT>
+__device__ inline v4f mfma_piece(v4u a, v4u b, v4f acc) {
+  if constexpr (DT == VR_DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[s]), __uint_as_float(b[s]), acc, 0, 0, 0);
+    return acc;
+  }
+}
+
+}  // namespace vr

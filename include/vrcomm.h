@@ -211,6 +211,7 @@ vrResult_t vr_comm_destroy(vrComm_t comm);
 #define VR_ASYNC_CAPACITY      0x2u
 #define VR_ASYNC_BAD_EXPERT    0x4u
 #define VR_ASYNC_LITMUS        0x8u
+#define VR_ASYNC_BAD_VALUE     0x10u /* a NaN or +inf logit: VR_ERR_DEVICE_CHECK */
 vrResult_t vr_comm_get_async_error(vrComm_t comm, vrResult_t* out, uint32_t* bits);
 
 /* Strong-signal litmus for the collectives (GIN page, strong and weak
@@ -575,6 +576,143 @@ vrResult_t vr_ring_exchange(vrComm_t comm, vrWindow_t send, vrWindow_t recv, siz
  * VR_ASYNC_TIMEOUT and ends the exchange. */
 vrResult_t vr_signal_pingpong(vrComm_t comm, vrWindow_t win, size_t off, size_t bytes, uint32_t iters,
                               uint32_t sig, uint32_t flags, void* stream);
+
+/* ---- the layers between the collectives ------------------------------------------------
+ * What a mixture-of-experts layer computes on either side of the dispatch and
+ * the combine: the router, the experts' matrix products (forward and backward)
+ * and, for a few tokens, the whole layer at once. All R ranks in one call,
+ * stream-ordered; no signals are applied. Tensors live in windows and are
+ * named by slices; arrays (ids, weights, row counts, the workspace) are plain
+ * device arrays. Rows are packed and row-major. Offsets need only the
+ * alignment of the element type; slices and rows that start on 16-byte
+ * boundaries run fastest. VR_DT_F32 and VR_DT_BF16; every sum is held in
+ * binary32 or wider, and bf16 outputs are rounded to nearest even once.
+ * Workspaces are the caller's: device memory of at least the stated bytes,
+ * 256-byte aligned, used until the call's work on the stream has run; calls
+ * that may overlap need workspaces of their own. Nothing is allocated, and
+ * every call may be captured into a graph as it is. */
+
+/* A tensor's place in a window: rank r's part starts `offset` bytes into its
+ * slice. window NULL: the optional tensor is absent (offset is ignored). */
+typedef struct {
+  vrWindow_t window;
+  uint64_t offset;
+} vrSlice;
+
+#define VR_ROUTE_RENORM  0x1u  /* weights of the chosen experts sum to 1 */
+
+/* Router: softmax over each token's expert logits and the K largest.
+ *   logits     rank s's [T][E] logits (slice, dtype)
+ *   topk_idx   device int32 [R][T][K]: the chosen experts, by falling logit,
+ *              ties to the lowest index; the routing vr_dispatch takes
+ *   weights    device float [R][T][K]: p[e] of the softmax over all E experts,
+ *              or with VR_ROUTE_RENORM p[e] / sum of the chosen p; what
+ *              vr_combine takes
+ * A logit of -inf masks its expert: it is never chosen. Where fewer than K
+ * experts are left the remaining entries are -1 with weight 0. A NaN or +inf
+ * logit is handled as -inf and sets VR_ASYNC_BAD_VALUE.
+ * K in 1..64, num_experts a multiple of R up to 1024, T < 65536. */
+vrResult_t vr_route(vrComm_t comm, vrSlice logits, int dtype, int T, int K, int num_experts,
+                    int32_t* topk_idx, float* weights, uint32_t flags, void* stream);
+
+/* Gradient of vr_route. topk_idx and weights as vr_route wrote them, dweights
+ * device float [R][T][K]; dlogits: rank s's [T][E] gradients (slice, dtype),
+ * every element written. With m = sum_k dweights[k] * weights[k] over the
+ * entries that are not -1: VR_ROUTE_RENORM: dlogits[e_k] = weights[k] *
+ * (dweights[k] - m), others 0 (logits are not read and may be absent);
+ * without: dlogits[j] = p[j] * (sum of dweights of entries naming j - m).
+ * Ids outside [-1, E) set VR_ASYNC_BAD_EXPERT and are skipped, as in
+ * vr_combine. dlogits may be the logits' own slice. */
+vrResult_t vr_route_backward(vrComm_t comm, vrSlice logits, int dtype, int T, int K, int num_experts,
+                             const int32_t* topk_idx, const float* weights, const float* dweights,
+                             vrSlice dlogits, uint32_t flags, void* stream);
+
+/* Activations of vr_linear and vr_moe_layer; GELU is the erf form. */
+#define VR_ACT_NONE   0x0u
+#define VR_ACT_RELU   0x1u
+#define VR_ACT_GELU   0x2u
+#define VR_ACT_SILU   0x3u
+#define VR_ACT_GATED  0x10u  /* or-ed in: act(first half of the columns) * second half */
+
+/* Shape of a linear layer on every rank: rows x in -> rows x out. With
+ * VR_ACT_GATED the weights have N = 2 * out rows (the gate's, then the
+ * linear half's), else N = out. groups: weight matrices per rank (local
+ * experts), 1 for a dense layer; 1..1024. rows up to 2^24, in and out up to
+ * 2^20. */
+typedef struct {
+  int dtype;
+  int rows;
+  int groups;
+  int in;
+  int out;
+  uint32_t act;
+} vrLinearShape;
+
+/* Device bytes of workspace a call needs; 0 also on invalid arguments. */
+size_t vr_linear_workspace_bytes(int nranks, const vrLinearShape* shape);
+size_t vr_linear_backward_workspace_bytes(int nranks, const vrLinearShape* shape);
+
+/* out = act(x w^T + bias) + residual on every rank.
+ *   x [rows][in], w [groups][N][in], out [rows][out]; optional: bias
+ *   [groups][N], residual [rows][out], preact [rows][N] (written: x w^T + bias
+ *   rounded to dtype, what the backward call reads)
+ *   group_rows  device int32 [R][groups]: group g's rows follow those of the
+ *               groups before it, as vr_dispatch lays them out and counts them
+ *               (recv_expert_counts). NULL only when groups is 1: all rows.
+ *               Rows past the last group are neither read nor written. A
+ *               negative count, or rows past `rows`, set VR_ASYNC_CAPACITY;
+ *               such rows are left out.
+ * residual may be out's own slice; no other ranges may overlap out or preact
+ * (VR_ERR_INVALID_ARGUMENT). */
+vrResult_t vr_linear(vrComm_t comm, const vrLinearShape* shape, vrSlice x, vrSlice w, vrSlice bias,
+                     vrSlice residual, const int32_t* group_rows, vrSlice out, vrSlice preact,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of vr_linear (residual's is dout itself). dout [rows][out];
+ * preact as the forward call wrote it, needed unless act is VR_ACT_NONE;
+ * wanted outputs: dx [rows][in] (rows past the last group are not written),
+ * dw [groups][N][in] and dbias [groups][N] (zeros for a group without rows);
+ * absent ones are not computed. bf16: the gradient of x w^T + bias is rounded
+ * to bf16 once before the two products; dbias sums it unrounded. Sums run in a
+ * fixed order: results do not change from run to run. */
+vrResult_t vr_linear_backward(vrComm_t comm, const vrLinearShape* shape, vrSlice dout, vrSlice x, vrSlice w,
+                              vrSlice preact, const int32_t* group_rows, vrSlice dx, vrSlice dw, vrSlice dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Shape of a mixture-of-experts layer on every rank: tokens rows of hidden
+ * elements, num_experts (all ranks') experts of hidden -> inner -> hidden.
+ * flags: VR_ROUTE_RENORM. At most VR_MOE_LAYER_MAX_TOKENS tokens over all
+ * ranks; topk 1..64 and at most num_experts. */
+#define VR_MOE_LAYER_MAX_TOKENS 64
+typedef struct {
+  int dtype;
+  int tokens;
+  int hidden;
+  int inner;
+  int num_experts;
+  int topk;
+  uint32_t act;
+  uint32_t flags;
+} vrMoeShape;
+
+size_t vr_moe_layer_workspace_bytes(int nranks, const vrMoeShape* shape);
+
+/* A whole mixture-of-experts layer for a few tokens (a decoding step): router,
+ * routing, expert products and weighted sum, without dispatch and combine. The
+ * experts read the tokens, and the tokens' sums the experts' outputs, straight
+ * from the other ranks' slices.
+ *   x [tokens][hidden]; router: device [num_experts][hidden] (dtype);
+ *   w_up [E/R][U][hidden], U = inner or, gated, 2 * inner; w_down
+ *   [E/R][hidden][inner] (rank d holds experts [d*E/R, (d+1)*E/R));
+ *   residual [tokens][hidden] optional, may be out's own slice
+ *   out [tokens][hidden] = residual + sum_k weights[k] * (w_down act(w_up x)),
+ *   summed in k order
+ *   topk_idx, weights: device [R][tokens][topk], written as vr_route would
+ *   from logits held in binary64 (a NaN or +inf logit sets VR_ASYNC_BAD_VALUE)
+ */
+vrResult_t vr_moe_layer(vrComm_t comm, const vrMoeShape* shape, vrSlice x, const void* router, vrSlice w_up,
+                        vrSlice w_down, vrSlice residual, vrSlice out, int32_t* topk_idx, float* weights,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

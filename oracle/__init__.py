@@ -33,6 +33,8 @@ Modules:
   ordering     relaxed-visibility model: enumerates every state the strong
                or weak signal rule allows and checks what an observer of a
                signal value may conclude
+  layers       binary64 definitions of the router, the linear layer and the
+               few-token expert layer, with their gradients
 
 Every function is pinned by tests under ``tests/`` (``-m "not gpu"``)
 against the pages' worked examples, closed forms, library routines,
@@ -53,4 +55,4 @@ sum and its own bf16 widening and rounding, pinned against torch), so its
 agreement with ``definitions`` checks the arithmetic as well as the data
 movement.
 """
-from . import primitives, definitions, protocol, ordering  # noqa: F401
+from . import primitives, definitions, protocol, ordering, layers  # noqa: F401
