@@ -97,8 +97,8 @@ __device__ inline void store4(char* p, uint64_t i, int n, const float* f) {
   }
 }
 
-template <int DT>
-__device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int col, v4f z0, v4f z1, bool gated) {
+template <int DT, int ACT, bool gated>
+__device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int col, v4f z0, v4f z1) {
   const int n = a.O - col;
   if (n <= 0) return;
   float g4[4], u4[4], y[4];
@@ -124,7 +124,7 @@ __device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int co
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    y[j] = act_value(g4[j], a.act);
+    y[j] = act_value<DT, ACT>(g4[j]);
     if (gated) y[j] *= u4[j];
   }
   if (a.residual.p[r]) {
@@ -136,141 +136,308 @@ __device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int co
   store4<DT>(a.out.p[r], (uint64_t)row * a.O + col, n, y);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// Workgroups of consecutive numbers run on the XCDs in turn; give each XCD
+// consecutive tiles, which share rows of a and b in its L2.
+__device__ inline int xcd_order(int b, int n) {
+  const int x = b & 7, q = n >> 3, rem = n & 7;
+  return x * q + min(x, rem) + (b >> 3);
+}
+
 // One BM x BN tile of out per workgroup; the waves' WM x WN parts stay in
 // registers. The matrix instructions take the b side (columns of out) as
 // their first operand, so a lane's four sums are four consecutive columns of
-// one row of out.
-template <int DT, int MODE, bool GATED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmArgs a) {
-  constexpr int kThreads = 64 * (BM / WM) * (BN / WN);
+// one row of out. While one 128-byte step of the contraction axis is
+// multiplied, the next is on its way into the other half of the LDS: straight
+// from global memory where rows start on 16 bytes (DIRECT), else through
+// registers, zero-filled past the ends.
+template <int DT, int MODE, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+struct Gemm {
+  static constexpr int kThreads = 64 * (BM / WM) * (BN / WN);
   using TA = Tile<DT, MODE != kDw, BM>;
   using TB = Tile<DT, MODE == kFwd, BN>;
-  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kK = TA::kK;
-  __shared__ __align__(16) char la[TA::kBytes];
-  __shared__ __align__(16) char lb[TB::kBytes];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  static constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kK = TA::kK;
+  static constexpr int kPA = TA::kPieces / kThreads, kPB = TB::kPieces / kThreads;
+  static constexpr int kMF = WM / 16, kNF = WN / 16;
+
+  struct Where {
+    const char *pa, *pb;  // the tile's rows of a and b at contraction index 0
+    uint64_t lda, ldb;    // bytes
+    int m0, mEnd, n0, N, O, K, width_a, width_b;
+  };
+
+  // Row of b behind tile row j (forward): gated, 16 gate columns, then the same 16 of the other half.
+  __device__ static int b_row(const Where& t, int j, bool* in) {
+    if constexpr (GATED) {
+      const int o = t.n0 / 2 + (j >> 5) * 16 + (j & 15);
+      *in = o < t.O;
+      return o + ((j >> 4) & 1) * t.O;
+    } else {
+      *in = t.n0 + j < t.N;
+      return t.n0 + j;
+    }
+  }
+
+  // Byte offsets of a thread's pieces from pa, pb; pieces outside are taken
+  // from a valid row or column (their products are not stored).
+  __device__ static void offsets(const Where& t, int tid, uint32_t* oa, uint32_t* ob) {
+#pragma unroll
+    for (int i = 0; i < kPA; ++i) {
+      const int id = i * kThreads + tid, sr = id / TA::kPerRow, c = (id % TA::kPerRow) ^ TA::swz(sr);
+      if constexpr (MODE != kDw) oa[i] = static_cast<uint32_t>(min(t.m0 + sr, t.mEnd - 1) - t.m0) * static_cast<uint32_t>(t.lda) + (c << 4);
+      else oa[i] = sr * static_cast<uint32_t>(t.lda) + min(t.m0 + c * kC, t.width_a - kC) * kES;
+    }
+#pragma unroll
+    for (int i = 0; i < kPB; ++i) {
+      const int id = i * kThreads + tid, sr = id / TB::kPerRow, c = (id % TB::kPerRow) ^ TB::swz(sr);
+      if constexpr (MODE == kFwd) {
+        bool in;
+        const int n = b_row(t, sr, &in);
+        ob[i] = 0;
+        if constexpr (GATED) {
+          const int o = min(n - ((sr >> 4) & 1) * t.O, t.O - 1);  // the second half's rows are t.O rows further on
+          ob[i] = static_cast<uint32_t>(o - t.n0 / 2) * static_cast<uint32_t>(t.ldb) + (c << 4);
+        } else {
+          ob[i] = static_cast<uint32_t>(min(n, t.N - 1) - t.n0) * static_cast<uint32_t>(t.ldb) + (c << 4);
+        }
+      } else {
+        ob[i] = sr * static_cast<uint32_t>(t.ldb) + min(t.n0 + c * kC, t.width_b - kC) * kES;
+      }
+    }
+  }
+
+  // Pieces of step k0 by registers, zero past the ends.
+  __device__ static void load(const Where& t, int tid, int k0, v4u* ra, v4u* rb) {
+#pragma unroll
+    for (int i = 0; i < kPA; ++i) {
+      const int id = i * kThreads + tid, sr = id / TA::kPerRow, c = (id % TA::kPerRow) ^ TA::swz(sr);
+      if constexpr (MODE != kDw) {
+        const int m = t.m0 + sr, k = k0 + c * kC;
+        ra[i] = load_piece<DT>(t.pa + (uint64_t)sr * t.lda + (uint64_t)k * kES, m < t.mEnd ? t.K - k : 0);
+      } else {
+        const int k = k0 + sr, m = t.m0 + c * kC;
+        ra[i] = load_piece<DT>(t.pa + (uint64_t)k * t.lda + (uint64_t)m * kES, k < t.K ? t.mEnd - m : 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPB; ++i) {
+      const int id = i * kThreads + tid, sr = id / TB::kPerRow, c = (id % TB::kPerRow) ^ TB::swz(sr);
+      if constexpr (MODE == kFwd) {
+        const int k = k0 + c * kC;
+        bool in;
+        const int n = b_row(t, sr, &in);
+        const int64_t from = n - (GATED ? t.n0 / 2 : t.n0);
+        rb[i] = load_piece<DT>(t.pb + from * static_cast<int64_t>(t.ldb) + (int64_t)k * kES, in ? t.K - k : 0);
+      } else {
+        const int k = k0 + sr, n = t.n0 + c * kC;
+        rb[i] = load_piece<DT>(t.pb + (uint64_t)k * t.ldb + (uint64_t)n * kES, k < t.K ? t.N - n : 0);
+      }
+    }
+  }
+  __device__ static void store(int tid, char* la, char* lb, const v4u* ra, const v4u* rb) {
+#pragma unroll
+    for (int i = 0; i < kPA; ++i) *reinterpret_cast<v4u*>(la + ((i * kThreads + tid) << 4)) = ra[i];
+#pragma unroll
+    for (int i = 0; i < kPB; ++i) *reinterpret_cast<v4u*>(lb + ((i * kThreads + tid) << 4)) = rb[i];
+  }
+
+  __device__ static void multiply(const char* la, const char* lb, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      v4u fa[kMF], fb[kNF];
+#pragma unroll
+      for (int i = 0; i < kNF; ++i) fb[i] = TB::frag(lb, wn + i * 16, ks, lane);
+#pragma unroll
+      for (int j = 0; j < kMF; ++j) fa[j] = TA::frag(la, wm + j * 16, ks, lane);
+#pragma unroll
+      for (int j = 0; j < kMF; ++j)
+#pragma unroll
+        for (int i = 0; i < kNF; ++i) acc[i][j] = mfma_piece<DT>(fb[i], fa[j], acc[i][j]);
+    }
+  }
+
+  // Start the loads of the whole step k1 into `to`.
+  __device__ static __forceinline__ void fetch(const Where& t, int k1, int tid, int wave, const uint32_t* oa,
+                                               const uint32_t* ob, char* to) {
+    const char* pa = t.pa + (MODE != kDw ? (uint64_t)k1 * kES : (uint64_t)k1 * t.lda);
+    const char* pb = t.pb + (MODE == kFwd ? (uint64_t)k1 * kES : (uint64_t)k1 * t.ldb);
+#pragma unroll
+    for (int i = 0; i < kPA; ++i)
+      __builtin_amdgcn_global_load_lds((global_void*)(pa + oa[i]), (lds_void*)(to + ((i * kThreads + wave * 64) << 4)),
+                                       16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kPB; ++i) {
+      uint64_t half = 0;  // gated: which half of the columns the piece's row is in
+      if constexpr (GATED) {
+        const int sr = (i * kThreads + tid) / TB::kPerRow;
+        half = ((sr >> 4) & 1) ? (uint64_t)t.O * t.ldb : 0;
+      }
+      __builtin_amdgcn_global_load_lds((global_void*)(pb + ob[i] + half),
+                                       (lds_void*)(to + TA::kBytes + ((i * kThreads + wave * 64) << 4)), 16, 0, 0);
+    }
+  }
+
+  // Multiply what is in `cur` while step k1 goes to `nxt` (if `more`). The two
+  // halves do not overlap (__restrict__): reads of one need not wait for loads
+  // into the other.
+  __device__ static __forceinline__ void step(const Where& t, int k1, bool more, int tid, int wave, const uint32_t* oa,
+                                              const uint32_t* ob, const char* __restrict__ cur,
+                                              char* __restrict__ nxt, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+    if constexpr (DIRECT) {
+      if (more) fetch(t, k1, tid, wave, oa, ob, nxt);
+      multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
+      meet();
+    } else {
+      v4u ra[kPA], rb[kPB];
+      load(t, tid, k1, ra, rb);  // nothing past the end
+      multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
+      store(tid, nxt, nxt + TA::kBytes, ra, rb);
+      __syncthreads();
+    }
+  }
+  // Own loads have landed and own reads are done, in every wave.
+  __device__ static __forceinline__ void meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+};
+
+template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmArgs a) {
+  using G = Gemm<DT, MODE, GATED, DIRECT, BM, BN, WM, WN>;
+  constexpr int kES = G::kES, kK = G::kK, kMF = G::kMF, kNF = G::kNF;
+  __shared__ __align__(16) char s0[G::TA::kBytes + G::TB::kBytes];
+  __shared__ __align__(16) char s1[G::TA::kBytes + G::TB::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave % (BM / WM)) * WM, wn = (wave / (BM / WM)) * WN;
 
   // the tile: rank, group, rows and columns
-  int b = blockIdx.x;
+  int b = xcd_order(blockIdx.x, gridDim.x);
   const int nti = b % a.nt;
   b /= a.nt;
-  int r, g, m0, mEnd, row0, K;
+  int r, g, row0;
+  typename G::Where t;
   if constexpr (MODE == kDw) {
     const int mti = b % a.mt;
     b /= a.mt;
     g = b % a.G;
     r = b / a.G;
-    const GroupTile t = find_group<true>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, 1, g, a.err);
-    row0 = t.first;
-    K = t.count;
-    m0 = mti * BM;
-    mEnd = a.M;
+    const GroupTile q = find_group<true>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, 1, g, a.err);
+    row0 = q.first;
+    t.K = q.count;
+    t.m0 = mti * BM;
+    t.mEnd = a.M;
   } else {
     const int slot = b % a.mt;
     r = b / a.mt;
-    const GroupTile t = find_group<false>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
-    if (t.g < 0) return;
-    g = t.g;
-    row0 = t.first;
-    K = a.K;
-    m0 = (slot - t.tile0) * BM;
-    mEnd = t.count;
+    const GroupTile q = find_group<false>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
+    if (q.g < 0) return;
+    g = q.g;
+    row0 = q.first;
+    t.K = a.K;
+    t.m0 = (slot - q.tile0) * BM;
+    t.mEnd = q.count;
   }
-  const int n0 = nti * BN;  // tile's first column of b; gated: BN / 2 columns of either half
-  const char* pa = a.a.p[r] + (uint64_t)row0 * a.lda * kES;
-  const char* pb = a.b.p[r] + (MODE == kDw ? (uint64_t)row0 * a.ldb : (uint64_t)g * a.b_group) * kES;
+  t.n0 = nti * BN;  // tile's first column of b; gated: BN / 2 columns of either half
+  t.N = a.N;
+  t.O = a.O;
+  t.lda = a.lda * kES;
+  t.ldb = a.ldb * kES;
+  t.width_a = static_cast<int>(a.lda);
+  t.width_b = static_cast<int>(a.ldb);
+  t.pa = a.a.p[r] + (uint64_t)row0 * t.lda + (MODE != kDw ? (uint64_t)t.m0 * t.lda : 0);
+  t.pb = a.b.p[r] + (MODE == kDw ? (uint64_t)row0 * t.ldb : (uint64_t)g * a.b_group * kES) +
+         (MODE == kFwd ? (uint64_t)(GATED ? t.n0 / 2 : t.n0) * t.ldb : 0);
 
-  v4f acc[WN / 16][WM / 16];
+  v4f acc[kNF][kMF];
 #pragma unroll
-  for (int i = 0; i < WN / 16; ++i)
+  for (int i = 0; i < kNF; ++i)
 #pragma unroll
-    for (int j = 0; j < WM / 16; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    for (int j = 0; j < kMF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  for (int k0 = 0; k0 < K; k0 += kK) {
-    // stage: registers, then LDS
-#pragma unroll
-    for (int i = 0; i < TA::kPieces / kThreads; ++i) {
-      const int id = i * kThreads + tid, sr = id / TA::kPerRow, c = (id % TA::kPerRow) ^ TA::swz(sr);
-      v4u v;
-      if constexpr (MODE != kDw) {
-        const int m = m0 + sr, k = k0 + c * kC;
-        v = load_piece<DT>(pa + ((uint64_t)m * a.lda + k) * kES, m < mEnd ? K - k : 0);
-      } else {
-        const int k = k0 + sr, m = m0 + c * kC;
-        v = load_piece<DT>(pa + ((uint64_t)k * a.lda + m) * kES, k < K ? mEnd - m : 0);
-      }
-      *reinterpret_cast<v4u*>(la + (id << 4)) = v;
+  uint32_t oa[G::kPA], ob[G::kPB];
+  // whole steps (DIRECT; the others zero-fill and take every step here), two at a time
+  const int steps = DIRECT ? t.K / kK : (t.K + kK - 1) / kK;
+  if (steps > 0) {
+    if constexpr (DIRECT) {
+      G::offsets(t, tid, oa, ob);
+      G::fetch(t, 0, tid, wave, oa, ob, s0);
+      G::meet();
+    } else {
+      v4u ra[G::kPA], rb[G::kPB];
+      G::load(t, tid, 0, ra, rb);
+      G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
+      __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < TB::kPieces / kThreads; ++i) {
-      const int id = i * kThreads + tid, sr = id / TB::kPerRow, c = (id % TB::kPerRow) ^ TB::swz(sr);
-      v4u v;
-      if constexpr (MODE == kFwd) {
-        const int k = k0 + c * kC;
-        int n = n0 + sr;
-        bool in = n < a.N;
-        if constexpr (GATED) {  // 16 gate columns, then the same 16 of the other half
-          const int o = n0 / 2 + (sr >> 5) * 16 + (sr & 15);
-          in = o < a.O;
-          n = o + ((sr >> 4) & 1) * a.O;
-        }
-        v = load_piece<DT>(pb + ((uint64_t)n * a.ldb + k) * kES, in ? K - k : 0);
-      } else {
-        const int k = k0 + sr, n = n0 + c * kC;
-        v = load_piece<DT>(pb + ((uint64_t)k * a.ldb + n) * kES, k < K ? a.N - n : 0);
-      }
-      *reinterpret_cast<v4u*>(lb + (id << 4)) = v;
+    int i = 0;
+    for (; i + 2 <= steps; i += 2) {
+      G::step(t, (i + 1) * kK, true, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+      G::step(t, (i + 2) * kK, i + 2 < steps, tid, wave, oa, ob, s1, s0, wm, wn, lane, acc);
     }
+    if (i < steps) G::step(t, t.K, false, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+  }
+  if (DIRECT && steps * kK < t.K) {  // the last, partial step: by registers, zero-filled
+    v4u ra[G::kPA], rb[G::kPB];
+    G::load(t, tid, steps * kK, ra, rb);
+    G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
     __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      v4u fa[WM / 16], fb[WN / 16];
-#pragma unroll
-      for (int j = 0; j < WM / 16; ++j) fa[j] = TA::frag(la, wm + j * 16, ks, lane);
-#pragma unroll
-      for (int i = 0; i < WN / 16; ++i) fb[i] = TB::frag(lb, wn + i * 16, ks, lane);
-#pragma unroll
-      for (int i = 0; i < WN / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < WM / 16; ++j) acc[i][j] = mfma_piece<DT>(fb[i], fa[j], acc[i][j]);
-    }
-    __syncthreads();
+    G::multiply(s0, s0 + G::TA::kBytes, wm, wn, lane, acc);
   }
 
   const int cq = (lane >> 4) * 4;
 #pragma unroll
-  for (int j = 0; j < WM / 16; ++j) {
-    const int m = m0 + wm + j * 16 + (lane & 15);
-    if (m >= mEnd) continue;
+  for (int j = 0; j < kMF; ++j) {
+    const int m = t.m0 + wm + j * 16 + (lane & 15);
+    if (m >= t.mEnd) continue;
 #pragma unroll
-    for (int i = 0; i < WN / 16; i += GATED ? 2 : 1) {
+    for (int i = 0; i < kNF; i += GATED ? 2 : 1) {
       if constexpr (MODE == kFwd) {
-        const int col = GATED ? n0 / 2 + (wn + i * 16) / 2 + cq : n0 + wn + i * 16 + cq;
-        epilogue<DT>(a, r, g, row0 + m, col, acc[i][j], acc[i + (GATED ? 1 : 0)][j], GATED);
+        const int col = GATED ? t.n0 / 2 + (wn + i * 16) / 2 + cq : t.n0 + wn + i * 16 + cq;
+        epilogue<DT, ACT, GATED>(a, r, g, row0 + m, col, acc[i][j], acc[i + (GATED ? 1 : 0)][j]);
       } else {
-        const int col = n0 + wn + i * 16 + cq;
+        const int col = t.n0 + wn + i * 16 + cq;
         float y[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) y[q] = acc[i][j][q];
         const uint64_t row = MODE == kDw ? (uint64_t)m : (uint64_t)(row0 + m);
-        store4<DT>(a.out.p[r] + (uint64_t)g * a.out_group * kES, row * a.N + col, a.N - col, y);
+        if (col < a.N) store4<DT>(a.out.p[r] + (uint64_t)g * a.out_group * kES, row * a.N + col, a.N - col, y);
       }
     }
   }
 }
 
-template <int DT, int MODE, bool GATED>
-vrResult_t launch_gemm(GemmArgs& a, hipStream_t st) {
-  constexpr int BM = 128, BN = 128;
+// Whether every row of the present parts of both operands starts on 16 bytes.
+bool rows_aligned(const GemmArgs& a, int es) {
+  uintptr_t v = (a.lda * es) | (a.ldb * es) | (a.b_group * es);
+  for (int r = 0; r < a.R; ++r) v |= reinterpret_cast<uintptr_t>(a.a.p[r]) | reinterpret_cast<uintptr_t>(a.b.p[r]);
+  return v % 16 == 0;
+}
+
+template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   if (MODE == kDw) a.mt = (a.M + BM - 1) / BM;
   else a.mt = a.counts ? a.rows / BM + a.G : (a.rows + BM - 1) / BM;
   a.nt = GATED ? (a.O + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
   const uint64_t grid = (uint64_t)a.R * (MODE == kDw ? a.G : 1) * a.mt * a.nt;
   if (!grid) return VR_OK;
   if (grid > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
-  hipLaunchKernelGGL((k_gemm<DT, MODE, GATED, BM, BN, 64, 64>), dim3(static_cast<uint32_t>(grid)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_gemm<DT, MODE, ACT, GATED, DIRECT, BM, BN, WM, WN>), dim3(static_cast<uint32_t>(grid)),
+                     dim3(64 * (BM / WM) * (BN / WN)), 0, st, a);
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+}
+
+template <int DT, int MODE, int ACT, bool GATED>
+vrResult_t launch_gemm(GemmArgs& a, hipStream_t st) {
+  if (!rows_aligned(a, Elem<DT>::kSize)) return launch_tiles<DT, MODE, ACT, GATED, false, 128, 128, 64, 64>(a, st);
+  if constexpr (DT == VR_DT_BF16) {
+    // 256 x 256 tiles once they fill the chip
+    const uint64_t m = MODE == kDw ? (uint64_t)a.M * a.G : (uint64_t)a.rows;
+    if ((uint64_t)a.R * m * a.N >= 200ull * 256 * 256) return launch_tiles<DT, MODE, ACT, GATED, true, 256, 256, 128, 64>(a, st);
+  }
+  return launch_tiles<DT, MODE, ACT, GATED, true, 128, 128, 64, 64>(a, st);
 }
 
 // ---- the gradient of z, and of the bias ---------------------------------------------------
@@ -329,7 +496,7 @@ __global__ __launch_bounds__(256) void k_dz(const DzArgs a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float y, s;
-        act_both(g[j], a.act, &y, &s);
+        act_both<DT>(g[j], a.act, &y, &s);
         if (GATED) {
           g[j] = d[j] * u[j] * s;
           u[j] = d[j] * y;
@@ -423,7 +590,11 @@ vrResult_t linear(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrS
   a.lda = a.ldb = s.in;
   a.b_group = (uint64_t)a.N * s.in;
   a.act = s.act;
-  return gated(s) ? launch_gemm<DT, kFwd, true>(a, st) : launch_gemm<DT, kFwd, false>(a, st);
+  vrResult_t e = VR_OK;
+  with_act(s.act, [&](auto act) {
+    e = gated(s) ? launch_gemm<DT, kFwd, act(), true>(a, st) : launch_gemm<DT, kFwd, act(), false>(a, st);
+  });
+  return e;
 }
 
 template <int DT>
@@ -477,7 +648,7 @@ vrResult_t linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dou
     a.b_group = (uint64_t)N * s.in;
     a.out = slice_tab(dx);
     a.K = N;
-    const vrResult_t e = launch_gemm<DT, kDx, false>(a, st);
+    const vrResult_t e = launch_gemm<DT, kDx, VR_ACT_NONE, false>(a, st);
     if (e != VR_OK) return e;
   }
   if (dw.window) {
@@ -485,7 +656,7 @@ vrResult_t linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dou
     a.out = slice_tab(dw);
     a.out_group = (uint64_t)N * s.in;
     a.M = N;
-    const vrResult_t e = launch_gemm<DT, kDw, false>(a, st);
+    const vrResult_t e = launch_gemm<DT, kDw, VR_ACT_NONE, false>(a, st);
     if (e != VR_OK) return e;
   }
   return VR_OK;

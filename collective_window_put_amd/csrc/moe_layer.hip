@@ -180,7 +180,7 @@ __global__ __launch_bounds__(1024) void k_moe_plan(const MoeArgs a) {
 }
 
 // h of 16 columns of one expert: 4 waves split the hidden axis.
-template <int DT, bool GATED>
+template <int DT, int ACT, bool GATED>
 __global__ __launch_bounds__(256) void k_moe_up(const MoeArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC;
   const int u = blockIdx.x;
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void k_moe_up(const MoeArgs a) {
     const int c = threadIdx.x & 15, t = threadIdx.x >> 4;
     if (t0 + t < count && c0 + c < a.I) {
       const float zg = (part[0][0][c][t] + part[1][0][c][t]) + (part[2][0][c][t] + part[3][0][c][t]);
-      float y = act_value(zg, a.act);
+      float y = act_value<DT, ACT>(zg);
       if (GATED) {
         constexpr int h = GATED ? 1 : 0;
         y *= (part[0][h][c][t] + part[1][h][c][t]) + (part[2][h][c][t] + part[3][h][c][t]);
@@ -313,8 +313,10 @@ void launch_dt(const MoeArgs& a, hipStream_t st) {
   else if (a.E <= 256) hipLaunchKernelGGL((k_moe_plan<4>), dim3(1), dim3(1024), 0, st, a);
   else hipLaunchKernelGGL((k_moe_plan<16>), dim3(1), dim3(1024), 0, st, a);
   const dim3 up(slots, (a.I + 15) / 16), down(slots, (a.H + 15) / 16);
-  if (a.act & VR_ACT_GATED) hipLaunchKernelGGL((k_moe_up<DT, true>), up, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((k_moe_up<DT, false>), up, dim3(256), 0, st, a);
+  with_act(a.act, [&](auto act) {
+    if (a.act & VR_ACT_GATED) hipLaunchKernelGGL((k_moe_up<DT, act(), true>), up, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_moe_up<DT, act(), false>), up, dim3(256), 0, st, a);
+  });
   hipLaunchKernelGGL((k_moe_down<DT>), down, dim3(256), 0, st, a);
   hipLaunchKernelGGL((k_moe_sum<DT>), dim3((a.H + 255) / 256, a.N), dim3(256), 0, st, a);
 }
