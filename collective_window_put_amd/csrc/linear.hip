@@ -136,8 +136,17 @@ __device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int co
   store4<DT>(a.out.p[r], (uint64_t)row * a.O + col, n, y);
 }
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void global_void;
+// 16 bytes per lane from base + off straight into the LDS at `to` + 16 * lane
+// (`to` the same in all lanes). In asm so that the compiler, which cannot tell
+// the two halves of the LDS apart across a loop, does not wait for it before
+// every LDS read: the caller waits for vmcnt and meets at a barrier instead.
+// There is no output register, and the address is read when it issues.
+__device__ inline void load_lds16(const char* base, uint32_t off, char* to) {
+  const uint32_t lds = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
+}
 
 // Workgroups of consecutive numbers run on the XCDs in turn; give each XCD
 // consecutive tiles, which share rows of a and b in its L2.
@@ -243,18 +252,26 @@ struct Gemm {
     for (int i = 0; i < kPB; ++i) *reinterpret_cast<v4u*>(lb + ((i * kThreads + tid) << 4)) = rb[i];
   }
 
+  // Half ks of a step: the fragments, and their products.
+  __device__ static __forceinline__ void frags(const char* la, const char* lb, int ks, int wm, int wn, int lane,
+                                               v4u* fa, v4u* fb) {
+#pragma unroll
+    for (int i = 0; i < kNF; ++i) fb[i] = TB::frag(lb, wn + i * 16, ks, lane);
+#pragma unroll
+    for (int j = 0; j < kMF; ++j) fa[j] = TA::frag(la, wm + j * 16, ks, lane);
+  }
+  __device__ static __forceinline__ void products(const v4u* fa, const v4u* fb, v4f (*acc)[kMF]) {
+#pragma unroll
+    for (int j = 0; j < kMF; ++j)
+#pragma unroll
+      for (int i = 0; i < kNF; ++i) acc[i][j] = mfma_piece<DT>(fb[i], fa[j], acc[i][j]);
+  }
   __device__ static void multiply(const char* la, const char* lb, int wm, int wn, int lane, v4f (*acc)[kMF]) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       v4u fa[kMF], fb[kNF];
-#pragma unroll
-      for (int i = 0; i < kNF; ++i) fb[i] = TB::frag(lb, wn + i * 16, ks, lane);
-#pragma unroll
-      for (int j = 0; j < kMF; ++j) fa[j] = TA::frag(la, wm + j * 16, ks, lane);
-#pragma unroll
-      for (int j = 0; j < kMF; ++j)
-#pragma unroll
-        for (int i = 0; i < kNF; ++i) acc[i][j] = mfma_piece<DT>(fb[i], fa[j], acc[i][j]);
+      frags(la, lb, ks, wm, wn, lane, fa, fb);
+      products(fa, fb, acc);
     }
   }
 
@@ -264,27 +281,20 @@ struct Gemm {
     const char* pa = t.pa + (MODE != kDw ? (uint64_t)k1 * kES : (uint64_t)k1 * t.lda);
     const char* pb = t.pb + (MODE == kFwd ? (uint64_t)k1 * kES : (uint64_t)k1 * t.ldb);
 #pragma unroll
-    for (int i = 0; i < kPA; ++i)
-      __builtin_amdgcn_global_load_lds((global_void*)(pa + oa[i]), (lds_void*)(to + ((i * kThreads + wave * 64) << 4)),
-                                       16, 0, 0);
+    for (int i = 0; i < kPA; ++i) load_lds16(pa, oa[i], to + ((i * kThreads + wave * 64) << 4));
 #pragma unroll
     for (int i = 0; i < kPB; ++i) {
-      uint64_t half = 0;  // gated: which half of the columns the piece's row is in
-      if constexpr (GATED) {
-        const int sr = (i * kThreads + tid) / TB::kPerRow;
-        half = ((sr >> 4) & 1) ? (uint64_t)t.O * t.ldb : 0;
-      }
-      __builtin_amdgcn_global_load_lds((global_void*)(pb + ob[i] + half),
-                                       (lds_void*)(to + TA::kBytes + ((i * kThreads + wave * 64) << 4)), 16, 0, 0);
+      const char* half = pb;
+      // gated: 8 pieces of a wave's 8 rows are in one block of 16, so in one half of the columns
+      if constexpr (GATED)
+        half += ((((i * kThreads + wave * 64) / TB::kPerRow) >> 4) & 1) ? (uint64_t)t.O * t.ldb : 0;
+      load_lds16(half, ob[i], to + TA::kBytes + ((i * kThreads + wave * 64) << 4));
     }
   }
 
-  // Multiply what is in `cur` while step k1 goes to `nxt` (if `more`). The two
-  // halves do not overlap (__restrict__): reads of one need not wait for loads
-  // into the other.
+  // Multiply what is in `cur` while step k1 goes to `nxt` (if `more`).
   __device__ static __forceinline__ void step(const Where& t, int k1, bool more, int tid, int wave, const uint32_t* oa,
-                                              const uint32_t* ob, const char* __restrict__ cur,
-                                              char* __restrict__ nxt, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+                                              const uint32_t* ob, const char* cur, char* nxt, int wm, int wn, int lane, v4f (*acc)[kMF]) {
     if constexpr (DIRECT) {
       if (more) fetch(t, k1, tid, wave, oa, ob, nxt);
       multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
@@ -297,6 +307,54 @@ struct Gemm {
       __syncthreads();
     }
   }
+  // Two groups of four waves, one wave of each per SIMD, a phase apart: while
+  // one reads its fragments of a half step from the LDS the other multiplies,
+  // so that the matrix units do not wait for the LDS. Phases end at barriers:
+  //   first group    R0(t) M0(t) R1(t) M1(t)  R0(t+1) ...
+  //   second group   M1(t-1) R0(t) M0(t) R1(t)  M1(t) ...
+  // In the phase of the first group's R0(t) every read of step t-1 is done:
+  // both groups then start loading step t+1 over it, and wait for it at the
+  // end of the phase of M1(t), before the first group's R0(t+1).
+  template <bool FIRST>
+  __device__ static __forceinline__ void phases(const Where& t, int steps, int tid, int wave, const uint32_t* oa,
+                                                const uint32_t* ob, char* s0, char* s1, int wm, int wn, int lane,
+                                                v4f (*acc)[kMF]) {
+    if (!FIRST) {
+      if (steps > 1) fetch(t, kK, tid, wave, oa, ob, s1);
+      barrier();
+    }
+    for (int i = 0; i < steps; ++i) {
+      char* cur = (i & 1) ? s1 : s0;
+      char* nxt = (i & 1) ? s0 : s1;
+      v4u fa[kMF], fb[kNF];
+      if (FIRST && i + 1 < steps) fetch(t, (i + 1) * kK, tid, wave, oa, ob, nxt);
+      frags(cur, cur + TA::kBytes, 0, wm, wn, lane, fa, fb);
+      lds_done();
+      barrier();
+      __builtin_amdgcn_s_setprio(1);
+      products(fa, fb, acc);
+      __builtin_amdgcn_s_setprio(0);
+      barrier();
+      frags(cur, cur + TA::kBytes, 1, wm, wn, lane, fa, fb);
+      lds_done();
+      if (!FIRST) wait_vmem();
+      barrier();
+      if (!FIRST && i + 2 < steps) fetch(t, (i + 2) * kK, tid, wave, oa, ob, cur);
+      __builtin_amdgcn_s_setprio(1);
+      products(fa, fb, acc);
+      __builtin_amdgcn_s_setprio(0);
+      if (FIRST) wait_vmem();
+      barrier();
+    }
+    if (FIRST) barrier();
+  }
+  __device__ static __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+  __device__ static __forceinline__ void barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   // Own loads have landed and own reads are done, in every wave.
   __device__ static __forceinline__ void meet() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -372,12 +430,17 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
       G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
       __syncthreads();
     }
+    if constexpr (DIRECT && G::kThreads == 512) {
+      if (wave < 4) G::template phases<true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+      else G::template phases<false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+    } else {
     int i = 0;
     for (; i + 2 <= steps; i += 2) {
       G::step(t, (i + 1) * kK, true, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
       G::step(t, (i + 2) * kK, i + 2 < steps, tid, wave, oa, ob, s1, s0, wm, wn, lane, acc);
     }
     if (i < steps) G::step(t, t.K, false, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+    }
   }
   if (DIRECT && steps * kK < t.K) {  // the last, partial step: by registers, zero-filled
     v4u ra[G::kPA], rb[G::kPB];

@@ -50,6 +50,12 @@ CASES = [  # R, rows, G, I, O, dtype, act, gated, bias, residual, off
     (1, 5, 1, 2048, 33, "f32", "gelu", False, True, False, 0),
     (2, 20, 3, 520, 96, "bf16", "silu", True, True, True, 0),
     (1, 64, 1, 1032, 64, "bf16", "relu", True, True, True, 0),
+    # large enough for the widest tiles: forward, dx, dw; contraction lengths of whole steps and with a remainder
+    (1, 3700, 1, 200, 3640, "bf16", "silu", False, True, True, 0),
+    (1, 3700, 1, 136, 1800, "bf16", "gelu", True, True, False, 0),
+    (2, 1900, 3, 3584, 72, "bf16", "none", False, False, False, 0),
+    (1, 330, 1, 3648, 3720, "bf16", "relu", False, True, False, 0),
+    (2, 150, 2, 1792, 1856, "bf16", "silu", True, False, False, 0),
 ]
 
 
