@@ -144,8 +144,11 @@ __device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int co
 __device__ inline void load_lds16(const char* base, uint32_t off, char* to) {
   const uint32_t lds = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to)));
+  const uint64_t at = reinterpret_cast<uintptr_t>(base);
+  const uint64_t uniform = (static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32))) << 32) |
+                           static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform) : "memory");
 }
 
 // Workgroups of consecutive numbers run on the XCDs in turn; give each XCD
