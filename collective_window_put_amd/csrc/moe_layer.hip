@@ -8,6 +8,13 @@
 // first operand of the matrix instructions, 16 rows to a wave, read straight
 // from HBM into registers; an expert's tokens, up to 16 at a time, are the
 // second, so an expert's weights are read once for its first 16 tokens.
+// Four launches: the routing (a workgroup per token), the up products, the
+// down products and the weighted sum. What a product needs of the routing it
+// works out again from the chosen ids: that costs a workgroup less than one
+// more launch costs the call. The sum has a launch of its own: by the last
+// workgroup of each column group to arrive at a counter it took 8 us more for
+// one token and 30 us more for 32 (coherent stores, an atomic and an acquire
+// for every workgroup of the down products).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,288 +26,386 @@ namespace {
 
 constexpr int kMaxPairs = VR_MOE_LAYER_MAX_TOKENS * 64;
 
-struct Plan {              // written by k_moe_plan
-  int used;                // experts with at least one entry
-  int pad[3];
-  int expert[1024];        // slot -> expert, ascending
-  int first[1025];         // slot -> first of its entries in pair[]
-  int pair[kMaxPairs];     // entry (token * K + k), by expert, ascending
-};
-
 struct MoeArgs {
   WinTab x, up, down, residual, out;
   const char* router;
   int32_t* topk;   // [R * T][K]
   float* weights;  // [R * T][K]
   uint32_t* err;
-  double* logits;  // [N][E]
-  Plan* plan;
-  float* h;        // [N * K][I]
+  double* logits;  // [N][E], or null: k_moe_route computes them
+  char* h;         // [N * K][ldh] binary32; bf16: two such arrays, of the value and of what its rounding left out
   float* y;        // [N * K][H]
-  int R, T, N, H, I, E, K, renorm;
+  uint64_t h_part; // bytes from the first array to the second
+  int R, T, N, H, I, E, K, ldh, renorm;
   uint32_t act;
 };
 
-__device__ inline double wave_sum_f64(double v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
-}
-__device__ inline double wave_max_f64(double v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmax(v, __shfl_xor(v, m));
-  return v;
-}
 template <int DT>
 __device__ inline double piece_f64(v4u v, int j) {
   if constexpr (DT == VR_DT_F32) return __uint_as_float(v[j]);
   else return __uint_as_float((j & 1) ? (v[j / 2] & 0xFFFF0000u) : (v[j / 2] << 16));
 }
-
-// logits[n][e]: a wave takes one expert and 4 tokens. Products of two
-// elements are exact in binary64; the choice of the K largest is then that of
-// the exact logits except within a few 2^-53.
+// A token's logits of experts e0 .. e0 + 3 into out[0 .. 3], by one wave.
+// Products of two elements are exact in binary64; the choice of the K largest
+// is then that of the exact logits except within a few 2^-53.
 template <int DT>
-__global__ __launch_bounds__(256) void k_moe_logits(const MoeArgs a) {
+__device__ inline void expert_logits(const MoeArgs& a, int n, int e0, double* out) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize;
-  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6), n0 = blockIdx.y * 4;
-  if (e >= a.E) return;
-  const char* w = a.router + (uint64_t)e * a.H * kES;
-  const char* x[4];
+  const int lane = static_cast<int>(lane_id());
+  const char* x = a.x.p[n / a.T] + (uint64_t)(n % a.T) * a.H * kES;
+  const char* w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = min(n0 + i, a.N - 1);
-    x[i] = a.x.p[n / a.T] + (uint64_t)(n % a.T) * a.H * kES;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = a.router + (uint64_t)min(e0 + i, a.E - 1) * a.H * kES;
   double s[4] = {0, 0, 0, 0};
-  for (int c = lane * kC; c < a.H; c += 64 * kC) {
-    const v4u wv = load_piece<DT>(w + (uint64_t)c * kES, a.H - c);
+  // four pieces a lane of each row in flight: the rows come from another
+  // XCD's L2 or from HBM, and a workgroup is alone with its token
+  for (int c0 = 0; c0 < a.H; c0 += 4 * 64 * kC) {
+    v4u xv[4], wv[4][4];
+    const int c = c0 + lane * kC;
+    if (c0 + 4 * 64 * kC <= a.H) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v4u xv = load_piece<DT>(x[i] + (uint64_t)c * kES, a.H - c);
+      for (int u = 0; u < 4; ++u) {
+        const uint64_t at = (uint64_t)(c + u * 64 * kC) * kES;
+        xv[u] = load_whole<DT>(x + at);
 #pragma unroll
-      for (int j = 0; j < kC; ++j) s[i] = fma(piece_f64<DT>(wv, j), piece_f64<DT>(xv, j), s[i]);
+        for (int i = 0; i < 4; ++i) wv[u][i] = load_whole<DT>(w[i] + at);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint64_t at = (uint64_t)(c + u * 64 * kC) * kES;
+        const int n = a.H - c - u * 64 * kC;
+        xv[u] = load_piece<DT>(x + at, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wv[u][i] = load_piece<DT>(w[i] + at, n);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const double xj = piece_f64<DT>(xv[u], j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = fma(piece_f64<DT>(wv[u][i], j), xj, s[i]);
+      }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s[i] = wave_sum_f64(s[i]);
-    if (lane == 0 && n0 + i < a.N) a.logits[(uint64_t)(n0 + i) * a.E + e] = s[i];
+    s[i] = wave_sum(s[i]);
+    if (lane == 0 && e0 + i < a.E) out[i] = s[i];
   }
 }
 
-// The routing of every token (a wave each, as in vr_route), then the experts'
-// entry lists. One workgroup.
-template <int V>
-__global__ __launch_bounds__(1024) void k_moe_plan(const MoeArgs a) {
-  __shared__ short ids[kMaxPairs];
-  __shared__ int offset[1024], slot[1024];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int n = wave; n < a.N; n += 16) {
-    double x[V], best = -INFINITY;
-    bool bad = false;
+// The logits of 16 experts and one token.
+template <int DT>
+__global__ __launch_bounds__(256) void k_moe_logits(const MoeArgs a) {
+  const int n = blockIdx.y, e0 = blockIdx.x * 16 + (threadIdx.x >> 6) * 4;
+  if (e0 < a.E) expert_logits<DT>(a, n, e0, a.logits + (uint64_t)n * a.E + e0);
+}
+
+// A workgroup routes one token: its waves compute the logits (unless
+// k_moe_logits has), the first chooses.
+template <int DT, int V>
+__global__ __launch_bounds__(1024) void k_moe_route(const MoeArgs a) {
+  __shared__ double own[64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x;
+  const double* logits = own;
+  if (a.logits) {
+    logits = a.logits + (uint64_t)n * a.E;
+  } else {
+    for (int e0 = wave * 4; e0 < a.E; e0 += 64) expert_logits<DT>(a, n, e0, own + e0);
+    __syncthreads();
+    if (wave) return;
+  }
+  // as vr_route, in binary64
+  double x_[V], best = -INFINITY;
+  bool bad = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = lane * V + j;
-      x[j] = c < a.E ? a.logits[(uint64_t)n * a.E + c] : -INFINITY;
-      if (!(x[j] < INFINITY)) {
-        x[j] = -INFINITY;
-        bad = true;
-      }
-      best = fmax(best, x[j]);
+  for (int j = 0; j < V; ++j) {
+    const int c = lane * V + j;
+    x_[j] = c < a.E ? logits[c] : -INFINITY;
+    if (!(x_[j] < INFINITY)) {
+      x_[j] = -INFINITY;
+      bad = true;
     }
-    if (ballot(bad) && lane == 0) atomic_or_u32(a.err, VR_ASYNC_BAD_VALUE);
-    const double top = wave_max_f64(best);
-    double whole = 0.0;
-    if (!a.renorm) {
-      if (top > -INFINITY) {
+    best = fmax(best, x_[j]);
+  }
+  if (ballot(bad) && lane == 0) atomic_or_u32(a.err, VR_ASYNC_BAD_VALUE);
+  const double top = wave_max(best);
+  double whole = 0.0;
+  if (!a.renorm) {
+    if (top > -INFINITY) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) whole += exp(x[j] - top);
-      }
-      whole = wave_sum_f64(whole);
+      for (int j = 0; j < V; ++j) whole += exp(x_[j] - top);
     }
-    double mine = -INFINITY;
-    int id = -1;
-    for (int k = 0; k < a.K; ++k) {
-      const double m = k ? wave_max_f64(best) : top;
-      if (!(m > -INFINITY)) break;
-      const int owner = __builtin_ctzll(ballot(best == m));
-      int j0 = 0;
+    whole = wave_sum(whole);
+  }
+  double mine = -INFINITY;
+  int id = -1;
+  for (int k = 0; k < a.K; ++k) {
+    const double m = k ? wave_max(best) : top;
+    if (!(m > -INFINITY)) break;
+    const int owner = __builtin_ctzll(ballot(best == m));
+    int j0 = 0;
 #pragma unroll
-      for (int j = V - 1; j >= 0; --j) j0 = x[j] == m ? j : j0;
-      const int col = owner * V + __builtin_amdgcn_readlane(j0, owner);
-      if (lane == k) {
-        id = col;
-        mine = m;
+    for (int j = V - 1; j >= 0; --j) j0 = x_[j] == m ? j : j0;
+    const int col = owner * V + __builtin_amdgcn_readlane(j0, owner);
+    if (lane == k) {
+      id = col;
+      mine = m;
+    }
+    if (lane == owner) {
+      best = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x_[j] = j == j0 ? -INFINITY : x_[j];
+        best = fmax(best, x_[j]);
       }
-      if (lane == owner) {
-        best = -INFINITY;
+    }
+  }
+  const double part = id >= 0 ? exp(mine - top) : 0.0;
+  if (a.renorm) whole = wave_sum(part);
+  if (lane < a.K) {
+    const int at = n * a.K + lane;
+    a.topk[at] = id;
+    a.weights[at] = id >= 0 ? static_cast<float>(part / whole) : 0.0f;
+  }
+}
+
+// The entries of the slot-th expert that has any, in order, into list (LDS; a
+// token names an expert once at most); returns their count, 0 when there is no
+// such expert. All threads of the workgroup call it.
+__device__ inline int find_expert(const MoeArgs& a, int slot, short* ids, uint32_t* bits, short* list, int* expert) {
+
+  const int tid = threadIdx.x, lane = tid & 63, pairs = a.N * a.K;
+  if (a.N == 1) {  // one token's experts all differ: the slot is the entry
+    *expert = a.topk[slot];
+    list[0] = static_cast<short>(slot);
+    __syncthreads();
+    return *expert >= 0;
+  }
+  if (tid < 32) bits[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < pairs; i += blockDim.x) {
+    const int id = a.topk[i];
+    ids[i] = static_cast<short>(id);
+    if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  const uint32_t word = lane < 32 ? bits[lane] : 0;
+  int sum = __popc(word);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[j] = j == j0 ? -INFINITY : x[j];
-          best = fmax(best, x[j]);
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up(sum, m);
+    if (lane >= m) sum += o;
+  }
+  const uint64_t past = ballot(lane < 32 && sum > slot);
+  if (!past) return 0;
+  const int at = __builtin_ctzll(past);
+  uint32_t w = __builtin_amdgcn_readlane(word, at);
+  for (int skip = slot - (__builtin_amdgcn_readlane(sum, at) - __popc(w)); skip > 0; --skip) w &= w - 1;
+  const int e = at * 32 + __builtin_ctz(w);
+  int count = 0;  // each wave writes the whole list, all the same
+  for (int i0 = 0; i0 < pairs; i0 += 64) {
+    const bool hit = i0 + lane < pairs && ids[i0 + lane] == e;
+    const uint64_t m = ballot(hit);
+    if (hit) list[count + __popcll(m & ((1ull << lane) - 1))] = static_cast<short>(i0 + lane);
+    count += __popcll(m);
+  }
+  __syncthreads();
+  *expert = e;
+  return count;
+}
+
+__device__ inline char* h_row(const MoeArgs& a, int pair, int es) { return a.h + (uint64_t)pair * a.ldh * es; }
+
+// h of 16 columns of one expert: 8 waves split the hidden axis.
+template <int DT, int ACT, bool GATED>
+__global__ __launch_bounds__(512) void k_moe_up(const MoeArgs a) {
+  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC, NW = GATED ? 2 : 1;
+  __shared__ short ids[kMaxPairs], list[VR_MOE_LAYER_MAX_TOKENS];
+  __shared__ uint32_t bits[32];
+  __shared__ float part[8][NW][16][17];
+  const int cols = (a.I + 15) / 16;
+  int e;
+  const int count = find_expert(a, blockIdx.x / cols, ids, bits, list, &e);
+  if (!count) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+  const int c0 = blockIdx.x % cols * 16, epr = a.E / a.R;
+  const char* w = a.up.p[e / epr] + (uint64_t)(e % epr) * (GATED ? 2 : 1) * a.I * a.H * kES;
+  const int col = min(c0 + i, a.I - 1);
+  const char* wr[NW];
+#pragma unroll
+  for (int h = 0; h < NW; ++h) wr[h] = w + ((uint64_t)h * a.I + col) * a.H * kES;
+  const int per = (a.H + 8 * kStep - 1) / (8 * kStep) * kStep;  // of the hidden axis, per wave
+  for (int t0 = 0; t0 < count; t0 += 16) {
+    const int n = list[min(t0 + i, count - 1)] / a.K;
+    const char* x[1] = {a.x.p[n / a.T] + (uint64_t)(n % a.T) * a.H * kES};
+    v4f z[NW][1];
+#pragma unroll
+    for (int h = 0; h < NW; ++h) z[h][0] = v4f{0, 0, 0, 0};
+    stream_products<DT, NW, 1, 4>(wr, x, wave * per, min(a.H, (wave + 1) * per), a.H, z);
+#pragma unroll
+    for (int h = 0; h < NW; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[wave][h][q * 4 + j][i] = z[h][0][j];
+    __syncthreads();
+    const int c = threadIdx.x & 15, t = threadIdx.x >> 4;
+    if (t < 16 && t0 + t < count && c0 + c < a.I) {
+      float s[NW];
+#pragma unroll
+      for (int h = 0; h < NW; ++h) {
+        s[h] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) s[h] += part[v][h][c][t];
+      }
+      float y = act_value<DT, ACT>(s[0]);
+      if (GATED) y *= s[NW - 1];
+      char* to = h_row(a, list[t0 + t], kES);
+      Elem<DT>::store(to, c0 + c, y);
+      // bf16: what the rounding left out; the two hold the value to 2^-16, far below the outputs' rounding
+      if (DT == VR_DT_BF16) {
+        const float hi = Elem<DT>::round(y);
+        Elem<DT>::store(to + a.h_part, c0 + c, fabsf(hi) < INFINITY ? y - hi : 0.0f);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// y of CG * 16 columns of one expert. 8 waves: CG groups of 16 columns by 8 / CG parts
+// of the inner axis. h goes through the LDS, once for all waves (read by each
+// wave from memory, it took two loads for every load of weights and the
+// kernel reached 2.8 TB/s); the weights go straight to registers, the first of
+// them already while h is staged.
+template <int DT, int CG>
+__global__ __launch_bounds__(512, 4) void k_moe_down(const MoeArgs a) {
+  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC, kPart = 8 / CG;
+  constexpr int kArr = DT == VR_DT_BF16 ? 2 : 1;       // arrays of h
+  constexpr int kRow = 2048 / kArr;                    // bytes of a staged row, of each array: 2 KB a token in all
+  constexpr int kK = kRow / kES, kPieces = kRow / 16;  // inner elements staged at a time
+  constexpr int U = 8;
+  __shared__ __align__(16) char hs[16 * kRow * kArr];
+  __shared__ short ids[kMaxPairs], list[VR_MOE_LAYER_MAX_TOKENS];
+  __shared__ uint32_t bits[32];
+  __shared__ float part[8][16][17];
+  const int cols = (a.H + CG * 16 - 1) / (CG * 16);
+  int e;
+  const int count = find_expert(a, blockIdx.x / cols, ids, bits, list, &e);
+  const int cb = blockIdx.x % cols;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+  const int c0 = (cb * CG + wave % CG) * 16, pt = wave / CG, epr = a.E / a.R;
+  if (count) {
+    const char* w = a.down.p[e / epr] + ((uint64_t)(e % epr) * a.H + min(c0 + i, a.H - 1)) * a.I * kES;
+    for (int t0 = 0; t0 < count; t0 += 16) {
+      const int rows = min(count - t0, 16);
+      v4f z[kArr];
+#pragma unroll
+      for (int h = 0; h < kArr; ++h) z[h] = v4f{0, 0, 0, 0};
+      for (int k0 = 0; k0 < a.I; k0 += kK) {
+        const int len = min(a.I - k0, kK), steps = (len + kStep - 1) / kStep;
+        const int per = (steps + kPart - 1) / kPart, s1 = min(steps, (pt + 1) * per);
+        v4u wv[U];
+        auto fetch = [&](int s) {  // steps [s, s + U) of the weights; past the end: the last, unused or zero-filled
+          const int k = k0 + s * kStep + q * kC;
+          if (k0 + (s + U) * kStep <= a.I) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              wv[u] = load_whole<DT>(w + (uint64_t)(k + u * kStep) * kES);
+          } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) wv[u] = load_piece<DT>(w + (uint64_t)(k + u * kStep) * kES, a.I - k - u * kStep);
+          }
+        };
+        int s = pt * per;
+        if (s < s1) fetch(s);
+        __syncthreads();  // the staged rows of the step before have been read
+        for (int id = tid; id < rows * kArr * kPieces; id += 512) {
+          const int p = id % kPieces, h = id / kPieces % kArr, t = id / (kPieces * kArr);
+          if (p * kC < len) {
+            const v4u v = load_piece<DT>(h_row(a, list[t0 + t], kES) + h * a.h_part + (uint64_t)(k0 + p * kC) * kES, len - p * kC);
+            *reinterpret_cast<v4u*>(hs + (t * kArr + h) * kRow + ((p ^ (t & 7)) << 4)) = v;
+          }
+        }
+        __syncthreads();
+        const int t = min(i, rows - 1);
+        while (s < s1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (s + u >= s1) break;
+            const int p = (s + u) * 4 + q;
+#pragma unroll
+            for (int h = 0; h < kArr; ++h) {
+              v4u hv = {0, 0, 0, 0};
+              if (p * kC < len) hv = *reinterpret_cast<const v4u*>(hs + (t * kArr + h) * kRow + ((p ^ (t & 7)) << 4));
+              z[h] = mfma_piece<DT>(wv[u], hv, z[h]);
+            }
+          }
+          s += U;
+          if (s < s1) fetch(s);
+        }
+      }
+      const v4f sum = kArr == 2 ? z[0] + z[kArr - 1] : z[0];
+      if (kPart == 1) {
+        if (i < rows) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c0 + q * 4 + j < a.H)
+              a.y[(uint64_t)list[t0 + i] * a.H + c0 + q * 4 + j] = sum[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[wave][q * 4 + j][i] = sum[j];
+        __syncthreads();
+        for (int v = tid; v < CG * 256; v += 512) {
+          const int c = v & 15, t = v >> 4 & 15, g = v >> 8, col = (cb * CG + g) * 16 + c;
+          if (t < rows && col < a.H) {
+            float y = 0.0f;
+#pragma unroll
+            for (int p = 0; p < kPart; ++p) y += part[p * CG + g][c][t];
+            a.y[(uint64_t)list[t0 + t] * a.H + col] = y;
+          }
         }
       }
     }
-    const double part = id >= 0 ? exp(mine - top) : 0.0;
-    if (a.renorm) whole = wave_sum_f64(part);
-    if (lane < a.K) {
-      const int at = n * a.K + lane;
-      a.topk[at] = id;
-      a.weights[at] = id >= 0 ? static_cast<float>(part / whole) : 0.0f;
-      ids[at] = static_cast<short>(id);
-    }
-  }
-  __syncthreads();
-  // thread e counts expert e's entries; then two sums over the experts
-  const int pairs = a.N * a.K;
-  int cnt = 0;
-  for (int i = 0; i < pairs; ++i) cnt += ids[i] == tid;
-  offset[tid] = cnt;
-  slot[tid] = cnt > 0;
-  __syncthreads();
-  for (int m = 1; m < 1024; m <<= 1) {
-    const int o = tid >= m ? offset[tid - m] : 0, s = tid >= m ? slot[tid - m] : 0;
-    __syncthreads();
-    offset[tid] += o;
-    slot[tid] += s;
-    __syncthreads();
-  }
-  if (cnt) {
-    const int u = slot[tid] - 1, first = offset[tid] - cnt;
-    a.plan->expert[u] = tid;
-    a.plan->first[u] = first;
-    for (int i = 0, k = first; i < pairs; ++i)
-      if (ids[i] == tid) a.plan->pair[k++] = i;
-  }
-  if (tid == 1023) {
-    a.plan->used = slot[1023];
-    a.plan->first[slot[1023]] = offset[1023];
   }
 }
 
-// h of 16 columns of one expert: 4 waves split the hidden axis.
-template <int DT, int ACT, bool GATED>
-__global__ __launch_bounds__(256) void k_moe_up(const MoeArgs a) {
-  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC;
-  const int u = blockIdx.x;
-  if (u >= a.plan->used) return;
-  const int e = a.plan->expert[u], first = a.plan->first[u], count = a.plan->first[u + 1] - first;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int c0 = blockIdx.y * 16, epr = a.E / a.R;
-  const int U = GATED ? 2 * a.I : a.I;
-  const char* w = a.up.p[e / epr] + (uint64_t)(e % epr) * U * a.H * kES;
-  const int col = min(c0 + i, a.I - 1);
-  const char* wg = w + (uint64_t)col * a.H * kES;
-  const char* wu = w + (uint64_t)(GATED ? a.I + col : col) * a.H * kES;
-  const int per = ((a.H + 4 * kStep - 1) / (4 * kStep)) * kStep;  // of the hidden axis, per wave
-  const int k1 = min(a.H, (wave + 1) * per);
-  __shared__ float part[4][GATED ? 2 : 1][16][17];
-  for (int t0 = 0; t0 < count; t0 += 16) {
-    const int pr = a.plan->pair[first + min(t0 + i, count - 1)], n = pr / a.K;
-    const char* x = a.x.p[n / a.T] + (uint64_t)(n % a.T) * a.H * kES;
-    v4f g = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int k = wave * per + q * kC; k - q * kC < k1; k += kStep) {
-      const v4u xv = load_piece<DT>(x + (uint64_t)k * kES, a.H - k);
-      g = mfma_piece<DT>(load_piece<DT>(wg + (uint64_t)k * kES, a.H - k), xv, g);
-      if (GATED) v = mfma_piece<DT>(load_piece<DT>(wu + (uint64_t)k * kES, a.H - k), xv, v);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      part[wave][0][q * 4 + j][i] = g[j];
-      if (GATED) part[wave][GATED ? 1 : 0][q * 4 + j][i] = v[j];
-    }
-    __syncthreads();
-    const int c = threadIdx.x & 15, t = threadIdx.x >> 4;
-    if (t0 + t < count && c0 + c < a.I) {
-      const float zg = (part[0][0][c][t] + part[1][0][c][t]) + (part[2][0][c][t] + part[3][0][c][t]);
-      float y = act_value<DT, ACT>(zg);
-      if (GATED) {
-        constexpr int h = GATED ? 1 : 0;
-        y *= (part[0][h][c][t] + part[1][h][c][t]) + (part[2][h][c][t] + part[3][h][c][t]);
-      }
-      a.h[(uint64_t)a.plan->pair[first + t0 + t] * a.I + c0 + c] = y;
-    }
-    __syncthreads();
-  }
-}
-
-// 8 binary32 values as the sum of two bf16 pieces (their error, 2^-16 of the
-// value, is far below the outputs' rounding).
-__device__ inline void split_piece(const float* f, v4u* hi, v4u* lo) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    (*hi)[j] = bf16_pack(f[2 * j], f[2 * j + 1]);
-    (*lo)[j] = bf16_pack(f[2 * j] - bf16lo((*hi)[j]), f[2 * j + 1] - bf16hi((*hi)[j]));
-  }
-}
-
-// y of 16 columns of one expert: 4 waves split the inner axis.
-template <int DT>
-__global__ __launch_bounds__(256) void k_moe_down(const MoeArgs a) {
-  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC;
-  const int u = blockIdx.x;
-  if (u >= a.plan->used) return;
-  const int e = a.plan->expert[u], first = a.plan->first[u], count = a.plan->first[u + 1] - first;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int c0 = blockIdx.y * 16, epr = a.E / a.R;
-  const char* w = a.down.p[e / epr] + ((uint64_t)(e % epr) * a.H + min(c0 + i, a.H - 1)) * a.I * kES;
-  const int per = ((a.I + 4 * kStep - 1) / (4 * kStep)) * kStep;
-  const int k1 = min(a.I, (wave + 1) * per);
-  __shared__ float part[4][16][17];
-  for (int t0 = 0; t0 < count; t0 += 16) {
-    const float* h = a.h + (uint64_t)a.plan->pair[first + min(t0 + i, count - 1)] * a.I;
-    v4f s = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int k = wave * per + q * kC; k - q * kC < k1; k += kStep) {
-      const v4u wv = load_piece<DT>(w + (uint64_t)k * kES, a.I - k);
-      if constexpr (DT == VR_DT_F32) {
-        s = mfma_piece<DT>(wv, load_piece<VR_DT_F32>(reinterpret_cast<const char*>(h + k), a.I - k), s);
-      } else {
-        v4u p[2], hi, lo;
-        p[0] = load_piece<VR_DT_F32>(reinterpret_cast<const char*>(h + k), a.I - k);
-        p[1] = load_piece<VR_DT_F32>(reinterpret_cast<const char*>(h + k + 4), a.I - k - 4);
-        split_piece(reinterpret_cast<const float*>(p), &hi, &lo);
-        s = mfma_piece<DT>(wv, hi, s);
-        s = mfma_piece<DT>(wv, lo, s);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[wave][q * 4 + j][i] = s[j];
-    __syncthreads();
-    const int c = threadIdx.x & 15, t = threadIdx.x >> 4;
-    if (t0 + t < count && c0 + c < a.H)
-      a.y[(uint64_t)a.plan->pair[first + t0 + t] * a.H + c0 + c] =
-          (part[0][c][t] + part[1][c][t]) + (part[2][c][t] + part[3][c][t]);
-    __syncthreads();
-  }
-}
-
+// out: each token's entries in k order.
 template <int DT>
 __global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
   const int n = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.H) return;
   const int s = n / a.T;
   float acc = 0.0f;
-  for (int k = 0; k < a.K; ++k)
-    if (a.topk[n * a.K + k] >= 0) acc += a.weights[n * a.K + k] * a.y[(uint64_t)(n * a.K + k) * a.H + c];
+#pragma unroll 8
+  for (int k = 0; k < a.K; ++k) {
+    const int p = n * a.K + k;
+    if (a.topk[p] >= 0) acc += a.weights[p] * a.y[(uint64_t)p * a.H + c];
+  }
   const uint64_t at = (uint64_t)(n % a.T) * a.H + c;
   if (a.residual.p[s]) acc += Elem<DT>::load(a.residual.p[s], at);
   Elem<DT>::store(a.out.p[s], at, acc);
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+// Whether the logits have a launch of their own, spread over the chip: beside
+// 8 us for a token's 64 experts of 2048 hidden elements in one workgroup it
+// saves nothing, beside 24 us for 256 experts it saves 11.
+bool logits_apart(const vrMoeShape& s) { return (uint64_t)s.num_experts * s.hidden > 1u << 18; }
+
 struct MoeLayout {
-  size_t logits, plan, h, y, total;
+  int ldh;
+  size_t logits, h, h_part, y, total;
 };
 MoeLayout layout(int R, const vrMoeShape& s) {
   MoeLayout l;
-  const size_t N = (size_t)R * s.tokens;
+  const size_t N = (size_t)R * s.tokens, es = s.dtype == VR_DT_F32 ? 4 : 2;
+  l.ldh = static_cast<int>((s.inner + 16 / es - 1) / (16 / es) * (16 / es));
   l.logits = 0;
-  l.plan = align256(N * s.num_experts * sizeof(double));
-  l.h = l.plan + align256(sizeof(Plan));
-  l.y = l.h + align256(N * s.topk * s.inner * sizeof(float));
+  l.h = logits_apart(s) ? align256(N * s.num_experts * sizeof(double)) : 0;
+  l.h_part = align256(N * s.topk * l.ldh * es);
+  l.y = l.h + (s.dtype == VR_DT_F32 ? 1 : 2) * l.h_part;
   l.total = l.y + align256(N * s.topk * s.hidden * sizeof(float));
   return l;
 }
@@ -308,16 +413,21 @@ MoeLayout layout(int R, const vrMoeShape& s) {
 template <int DT>
 void launch_dt(const MoeArgs& a, hipStream_t st) {
   const int slots = std::min(a.N * a.K, a.E);
-  hipLaunchKernelGGL((k_moe_logits<DT>), dim3((a.E + 3) / 4, (a.N + 3) / 4), dim3(256), 0, st, a);
-  if (a.E <= 64) hipLaunchKernelGGL((k_moe_plan<1>), dim3(1), dim3(1024), 0, st, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((k_moe_plan<4>), dim3(1), dim3(1024), 0, st, a);
-  else hipLaunchKernelGGL((k_moe_plan<16>), dim3(1), dim3(1024), 0, st, a);
-  const dim3 up(slots, (a.I + 15) / 16), down(slots, (a.H + 15) / 16);
+  const int threads = a.logits ? 64 : 1024;
+  if (a.logits) hipLaunchKernelGGL((k_moe_logits<DT>), dim3((a.E + 15) / 16, a.N), dim3(256), 0, st, a);
+  if (a.E <= 64) hipLaunchKernelGGL((k_moe_route<DT, 1>), dim3(a.N), dim3(threads), 0, st, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((k_moe_route<DT, 4>), dim3(a.N), dim3(threads), 0, st, a);
+  else hipLaunchKernelGGL((k_moe_route<DT, 16>), dim3(a.N), dim3(threads), 0, st, a);
+  const dim3 up(slots * ((a.I + 15) / 16));
   with_act(a.act, [&](auto act) {
-    if (a.act & VR_ACT_GATED) hipLaunchKernelGGL((k_moe_up<DT, act(), true>), up, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_moe_up<DT, act(), false>), up, dim3(256), 0, st, a);
+    if (a.act & VR_ACT_GATED) hipLaunchKernelGGL((k_moe_up<DT, act(), true>), up, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((k_moe_up<DT, act(), false>), up, dim3(512), 0, st, a);
   });
-  hipLaunchKernelGGL((k_moe_down<DT>), down, dim3(256), 0, st, a);
+  // as many columns to a workgroup as leave the chip four of them per compute unit
+  const auto groups = [&](int cg) { return slots * ((a.H + cg * 16 - 1) / (cg * 16)); };
+  if (groups(8) >= 1024) hipLaunchKernelGGL((k_moe_down<DT, 8>), dim3(groups(8)), dim3(512), 0, st, a);
+  else if (groups(4) >= 512) hipLaunchKernelGGL((k_moe_down<DT, 4>), dim3(groups(4)), dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((k_moe_down<DT, 2>), dim3(groups(2)), dim3(512), 0, st, a);
   hipLaunchKernelGGL((k_moe_sum<DT>), dim3((a.H + 255) / 256, a.N), dim3(256), 0, st, a);
 }
 
@@ -339,9 +449,10 @@ vrResult_t launch_moe_layer(vrComm* c, const vrMoeShape& s, const vrSlice& x, co
   a.topk = topk;
   a.weights = weights;
   a.err = c->err;
-  a.logits = reinterpret_cast<double*>(ws + l.logits);
-  a.plan = reinterpret_cast<Plan*>(ws + l.plan);
-  a.h = reinterpret_cast<float*>(ws + l.h);
+  a.logits = logits_apart(s) ? reinterpret_cast<double*>(ws + l.logits) : nullptr;
+  a.h = ws + l.h;
+  a.h_part = l.h_part;
+  a.ldh = l.ldh;
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.R = c->nranks;
   a.T = s.tokens;

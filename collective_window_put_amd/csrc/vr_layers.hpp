@@ -157,16 +157,69 @@ inline void with_act(uint32_t act, F f) {
   }
 }
 
-// ---- wave reductions (all 64 lanes; every lane gets the result) --------------------
+// ---- wave reductions ------------------------------------------------------------------
+// Lane l's partner in step S of a reduction, over vector instructions alone
+// (no trip through the LDS: six steps of a maximum took 0.5 us that way, and
+// take 0.05 us this way): lanes 1 and 2 apart, then mirrored in 8 and in 16
+// lanes (by then 4 and 8 lanes hold equal values), then rows 16 and 32 apart.
+// The two values of a step are the same in both partners, so every lane gets
+// the same result, bit for bit.
+template <int S>
+__device__ inline void dpp_pair(uint32_t v, uint32_t* a, uint32_t* b) {
+  if constexpr (S < 4) {
+    constexpr int kCtrl[4] = {0xB1, 0x4E, 0x141, 0x140};  // quad_perm 1,0,3,2 and 2,3,0,1; row_half_mirror; row_mirror
+    *a = v;
+    *b = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), kCtrl[S], 0xF, 0xF, false));
+  } else {
+    v2u r;
+    if constexpr (S == 4) r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    else r = __builtin_bit_cast(v2u, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    *a = r[0];
+    *b = r[1];
+  }
+}
+template <int S, class T>
+__device__ inline void lane_pair(T v, T* a, T* b) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t x, y;
+    dpp_pair<S>(__builtin_bit_cast(uint32_t, v), &x, &y);
+    *a = __builtin_bit_cast(T, x);
+    *b = __builtin_bit_cast(T, y);
+  } else {
+    const v2u w = __builtin_bit_cast(v2u, v);
+    v2u x, y;
+    uint32_t x0, x1, y0, y1;
+    dpp_pair<S>(w[0], &x0, &y0);
+    dpp_pair<S>(w[1], &x1, &y1);
+    x = v2u{x0, x1};
+    y = v2u{y0, y1};
+    *a = __builtin_bit_cast(T, x);
+    *b = __builtin_bit_cast(T, y);
+  }
+}
+// Steps [0, STEPS): 4 reduce rows of 16 lanes, 6 the wave; all lanes of a row
+// (the wave) get the result.
+template <int STEPS, int S = 0, class T, class F>
+__device__ inline T lane_reduce(T v, F f) {
+  if constexpr (S < STEPS) {
+    T a, b;
+    lane_pair<S>(v, &a, &b);
+    return lane_reduce<STEPS, S + 1>(f(a, b), f);
+  } else {
+    return v;
+  }
+}
 __device__ inline float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  return lane_reduce<6>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+  return lane_reduce<6>(v, [](float a, float b) { return a + b; });
+}
+__device__ inline double wave_max(double v) {
+  return lane_reduce<6>(v, [](double a, double b) { return fmax(a, b); });
+}
+__device__ inline double wave_sum(double v) {
+  return lane_reduce<6>(v, [](double a, double b) { return a + b; });
 }
 
 // ---- groups -------------------------------------------------------------------------
@@ -229,13 +282,20 @@ __device__ inline GroupTile find_group(const int32_t* counts, int G, int rows, i
 }
 
 // ---- 16-byte pieces of a row -----------------------------------------------------------
+// A whole piece; any element alignment.
+template <int DT>
+__device__ inline v4u load_whole(const char* p) {
+  v4u v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(p, Elem<DT>::kSize), 16);
+  return v;
+}
 // The piece's first n elements (n may be past either end of the piece), the
 // others 0. Any element alignment.
 template <int DT>
 __device__ inline v4u load_piece(const char* p, int n) {
   v4u v = {0, 0, 0, 0};
   if (n >= Elem<DT>::kChunk) {
-    __builtin_memcpy(&v, __builtin_assume_aligned(p, Elem<DT>::kSize), 16);
+    v = load_whole<DT>(p);
   } else if (n > 0) {
 #pragma unroll
     for (int j = 0; j < Elem<DT>::kChunk - 1; ++j) {
@@ -263,6 +323,46 @@ __device__ inline v4f mfma_piece(v4u a, v4u b, v4f acc) {
     for (int s = 0; s < 4; ++s)
       acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[s]), __uint_as_float(b[s]), acc, 0, 0, 0);
     return acc;
+  }
+}
+
+
+// acc[i][j] += w[i] . x[j] over contraction elements [k, k1), of which K exist:
+// the lane's row of each of NW 16-row blocks of weights and NX of tokens, all
+// read straight into registers, U steps of loads in flight. k is a multiple of
+// the step. For products bound by the weights' bytes: nothing is shared
+// through the LDS, so the loads never wait for a barrier.
+template <int DT, int NW, int NX, int U>
+__device__ inline void stream_products(const char* const* w, const char* const* x, int k, int k1, int K,
+                                       v4f (*acc)[NX]) {
+  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC;
+  const int q = (lane_id() >> 4) * kC;
+  v4u wv[U][NW], xv[U][NX];
+  auto use = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+#pragma unroll
+      for (int j = 0; j < NX; ++j) acc[i][j] = mfma_piece<DT>(wv[u][i], xv[u][j], acc[i][j]);
+  };
+  for (; k + U * kStep <= min(k1, K); k += U * kStep) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint64_t at = (uint64_t)(k + u * kStep + q) * kES;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) wv[u][i] = load_whole<DT>(w[i] + at);
+#pragma unroll
+      for (int j = 0; j < NX; ++j) xv[u][j] = load_whole<DT>(x[j] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) use(u);
+  }
+  for (; k < k1; k += kStep) {
+    const uint64_t at = (uint64_t)(k + q) * kES;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) wv[0][i] = load_piece<DT>(w[i] + at, K - k - q);
+#pragma unroll
+    for (int j = 0; j < NX; ++j) xv[0][j] = load_piece<DT>(x[j] + at, K - k - q);
+    use(0);
   }
 }
 
