@@ -136,6 +136,89 @@ __device__ inline void epilogue(const GemmArgs& a, int r, int g, int row, int co
   store4<DT>(a.out.p[r], (uint64_t)row * a.O + col, n, y);
 }
 
+// 4 elements as they lie in memory.
+template <int DT> struct Raw4 { typedef v4u T; };
+template <> struct Raw4<VR_DT_BF16> { typedef v2u T; };
+template <int DT>
+__device__ inline typename Raw4<DT>::T load_raw4(const char* p) {
+  typename Raw4<DT>::T v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(p, Elem<DT>::kSize), sizeof(v));
+  return v;
+}
+template <int DT>
+__device__ inline v4f from_raw4(typename Raw4<DT>::T v) {
+  if constexpr (DT == VR_DT_F32) return __builtin_bit_cast(v4f, v);
+  else return v4f{bf16lo(v[0]), bf16hi(v[0]), bf16lo(v[1]), bf16hi(v[1])};
+}
+
+// Epilogue of a wave's part of a tile that has all its columns: NF x MF
+// fragments from column c0 and row m0 (of the group; rows up to mEnd). Loads
+// are issued many rows ahead: out might be residual's own slice, so the
+// compiler keeps their order, and a fragment at a time each load's latency was
+// waited for in turn (82 of the 300 us of a dense 8192 x 4096 x 4096
+// product).
+template <int DT, int ACT, bool GATED, int NF, int MF>
+__device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0, int m0, int mEnd, int c0, int lane,
+                                      const v4f (*acc)[MF]) {
+  constexpr int kES = Elem<DT>::kSize, NO = GATED ? NF / 2 : NF, S = GATED ? 2 : 1;
+  const int m1 = m0 + (lane & 15), col = c0 + (lane >> 4) * 4;
+  // rows whose residual is held at once: all of a small tile's, 32 registers
+  constexpr int kRows = MF <= 4 ? MF : 4;
+  typename Raw4<DT>::T bias[NO][S], res[kRows][NO];
+  const char* pb = a.bias.p[r];
+  const char* pr = a.residual.p[r];
+  char* pz = a.preact.p[r];
+  if (pb) {
+    pb += ((uint64_t)g * a.N + col) * kES;
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+      for (int h = 0; h < S; ++h) bias[i][h] = load_raw4<DT>(pb + (uint64_t)(h * a.O + i * 16) * kES);
+  }
+#pragma unroll
+  for (int j0 = 0; j0 < MF; j0 += kRows) {
+    if (pr) {
+#pragma unroll
+      for (int v = 0; v < kRows; ++v)
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+          res[v][i] = load_raw4<DT>(pr + ((uint64_t)(row0 + min(m1 + (j0 + v) * 16, mEnd - 1)) * a.O + col + i * 16) * kES);
+    }
+#pragma unroll
+    for (int v = 0; v < kRows; ++v) {
+      const uint64_t row = row0 + m1 + (j0 + v) * 16;
+      if (m1 + (j0 + v) * 16 < mEnd) {
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          float z[S][4], y[4];
+#pragma unroll
+          for (int h = 0; h < S; ++h) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) z[h][q] = acc[i * S + h][j0 + v][q];
+            if (pb) {
+              const v4f f = from_raw4<DT>(bias[i][h]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) z[h][q] += f[q];
+            }
+            if (pz) store_n<DT, 4>(pz, row * a.N + h * a.O + col + i * 16, z[h]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            y[q] = act_value<DT, ACT>(z[0][q]);
+            if (GATED) y[q] *= z[S - 1][q];
+          }
+          if (pr) {
+            const v4f f = from_raw4<DT>(res[v][i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] += f[q];
+          }
+          store_n<DT, 4>(a.out.p[r], row * a.O + col + i * 16, y);
+        }
+      }
+    }
+  }
+}
+
 // 16 bytes per lane from base + off straight into the LDS at `to` + 16 * lane
 // (`to` the same in all lanes). In asm so that the compiler, which cannot tell
 // the two halves of the LDS apart across a loop, does not wait for it before
@@ -165,7 +248,7 @@ __device__ inline int xcd_order(int b, int n) {
 // multiplied, the next is on its way into the other half of the LDS: straight
 // from global memory where rows start on 16 bytes (DIRECT), else through
 // registers, zero-filled past the ends.
-template <int DT, int MODE, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+template <int DT, int MODE, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 struct Gemm {
   static constexpr int kThreads = 64 * (BM / WM) * (BN / WN);
   using TA = Tile<DT, MODE != kDw, BM>;
@@ -173,6 +256,7 @@ struct Gemm {
   static constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kK = TA::kK;
   static constexpr int kPA = TA::kPieces / kThreads, kPB = TB::kPieces / kThreads;
   static constexpr int kMF = WM / 16, kNF = WN / 16;
+  static constexpr int kStage = TA::kBytes + TB::kBytes, kStages = !DIRECT || kThreads == 512 ? 2 : STAGES;
 
   struct Where {
     const char *pa, *pb;  // the tile's rows of a and b at contraction index 0
@@ -180,8 +264,82 @@ struct Gemm {
     int m0, mEnd, n0, N, O, K, width_a, width_b;
   };
 
+  struct Spot {
+    Where t;
+    int r, g, row0;
+  };
+  // Tile b of the launch: column tiles, then row tiles, then groups (kDw) and
+  // ranks. False when there is no such tile.
+  __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s) {
+    Where& t = s->t;
+    const int nti = b % a.nt;
+    b /= a.nt;
+    const int slot = b % a.mt;
+    b /= a.mt;
+    if constexpr (MODE == kDw) {
+      s->g = b % a.G;
+      s->r = b / a.G;
+      const GroupTile q = find_group<true>(a.counts ? a.counts + (size_t)s->r * a.G : nullptr, a.G, a.rows, 1, s->g, a.err);
+      s->row0 = q.first;
+      t.K = q.count;
+      t.m0 = slot * BM;
+      t.mEnd = a.M;
+    } else {
+      s->r = b;
+      const GroupTile q = find_group<false>(a.counts ? a.counts + (size_t)s->r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
+      if (q.g < 0) return false;
+      s->g = q.g;
+      s->row0 = q.first;
+      t.K = a.K;
+      t.m0 = (slot - q.tile0) * BM;
+      t.mEnd = q.count;
+    }
+    t.n0 = nti * BN;  // tile's first column of b; gated: BN / 2 columns of either half
+    t.N = a.N;
+    t.O = a.O;
+    t.lda = a.lda * kES;
+    t.ldb = a.ldb * kES;
+    t.width_a = static_cast<int>(a.lda);
+    t.width_b = static_cast<int>(a.ldb);
+    t.pa = a.a.p[s->r] + (uint64_t)s->row0 * t.lda + (MODE != kDw ? (uint64_t)t.m0 * t.lda : 0);
+    t.pb = a.b.p[s->r] + (MODE == kDw ? (uint64_t)s->row0 * t.ldb : (uint64_t)s->g * a.b_group * kES) +
+           (MODE == kFwd ? (uint64_t)(GATED ? t.n0 / 2 : t.n0) * t.ldb : 0);
+    return true;
+  }
+
+  template <int ACT>
+  __device__ static __forceinline__ void finish(const GemmArgs& a, const Spot& s, int wm, int wn, int lane, const v4f (*acc)[kMF]) {
+    const Where& t = s.t;
+    if constexpr (MODE == kFwd) {
+      if (GATED ? t.n0 / 2 + BN / 2 <= a.O : t.n0 + BN <= a.N) {
+        epilogue_whole<DT, ACT, GATED, kNF, kMF>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, GATED ? (t.n0 + wn) / 2 : t.n0 + wn, lane, acc);
+        return;
+      }
+    }
+    const int cq = (lane >> 4) * 4;
+#pragma unroll
+    for (int j = 0; j < kMF; ++j) {
+      const int m = t.m0 + wm + j * 16 + (lane & 15);
+      if (m >= t.mEnd) continue;
+#pragma unroll
+      for (int i = 0; i < kNF; i += GATED ? 2 : 1) {
+        if constexpr (MODE == kFwd) {
+          const int col = GATED ? t.n0 / 2 + (wn + i * 16) / 2 + cq : t.n0 + wn + i * 16 + cq;
+          epilogue<DT, ACT, GATED>(a, s.r, s.g, s.row0 + m, col, acc[i][j], acc[i + (GATED ? 1 : 0)][j]);
+        } else {
+          const int col = t.n0 + wn + i * 16 + cq;
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = acc[i][j][q];
+          const uint64_t row = MODE == kDw ? (uint64_t)m : (uint64_t)(s.row0 + m);
+          if (col < a.N) store4<DT>(a.out.p[s.r] + (uint64_t)s.g * a.out_group * kES, row * a.N + col, a.N - col, y);
+        }
+      }
+    }
+  }
+
   // Row of b behind tile row j (forward): gated, 16 gate columns, then the same 16 of the other half.
-  __device__ static int b_row(const Where& t, int j, bool* in) {
+  __device__ static __forceinline__ int b_row(const Where& t, int j, bool* in) {
     if constexpr (GATED) {
       const int o = t.n0 / 2 + (j >> 5) * 16 + (j & 15);
       *in = o < t.O;
@@ -194,7 +352,7 @@ struct Gemm {
 
   // Byte offsets of a thread's pieces from pa, pb; pieces outside are taken
   // from a valid row or column (their products are not stored).
-  __device__ static void offsets(const Where& t, int tid, uint32_t* oa, uint32_t* ob) {
+  __device__ static __forceinline__ void offsets(const Where& t, int tid, uint32_t* oa, uint32_t* ob) {
 #pragma unroll
     for (int i = 0; i < kPA; ++i) {
       const int id = i * kThreads + tid, sr = id / TA::kPerRow, c = (id % TA::kPerRow) ^ TA::swz(sr);
@@ -221,7 +379,7 @@ struct Gemm {
   }
 
   // Pieces of step k0 by registers, zero past the ends.
-  __device__ static void load(const Where& t, int tid, int k0, v4u* ra, v4u* rb) {
+  __device__ static __forceinline__ void load(const Where& t, int tid, int k0, v4u* ra, v4u* rb) {
 #pragma unroll
     for (int i = 0; i < kPA; ++i) {
       const int id = i * kThreads + tid, sr = id / TA::kPerRow, c = (id % TA::kPerRow) ^ TA::swz(sr);
@@ -248,7 +406,7 @@ struct Gemm {
       }
     }
   }
-  __device__ static void store(int tid, char* la, char* lb, const v4u* ra, const v4u* rb) {
+  __device__ static __forceinline__ void store(int tid, char* la, char* lb, const v4u* ra, const v4u* rb) {
 #pragma unroll
     for (int i = 0; i < kPA; ++i) *reinterpret_cast<v4u*>(la + ((i * kThreads + tid) << 4)) = ra[i];
 #pragma unroll
@@ -269,7 +427,7 @@ struct Gemm {
 #pragma unroll
       for (int i = 0; i < kNF; ++i) acc[i][j] = mfma_piece<DT>(fb[i], fa[j], acc[i][j]);
   }
-  __device__ static void multiply(const char* la, const char* lb, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+  __device__ static __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn, int lane, v4f (*acc)[kMF]) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       v4u fa[kMF], fb[kNF];
@@ -295,20 +453,34 @@ struct Gemm {
     }
   }
 
-  // Multiply what is in `cur` while step k1 goes to `nxt` (if `more`).
-  __device__ static __forceinline__ void step(const Where& t, int k1, bool more, int tid, int wave, const uint32_t* oa,
-                                              const uint32_t* ob, const char* cur, char* nxt, int wm, int wn, int lane, v4f (*acc)[kMF]) {
-    if constexpr (DIRECT) {
-      if (more) fetch(t, k1, tid, wave, oa, ob, nxt);
-      multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
-      meet();
-    } else {
-      v4u ra[kPA], rb[kPB];
-      load(t, tid, k1, ra, rb);  // nothing past the end
-      multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
-      store(tid, nxt, nxt + TA::kBytes, ra, rb);
-      __syncthreads();
+  // Multiply what is in `cur` while step k1 goes to `nxt` by registers.
+  __device__ static __forceinline__ void step(const Where& t, int k1, int tid, const char* cur, char* nxt, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+    v4u ra[kPA], rb[kPB];
+    load(t, tid, k1, ra, rb);  // nothing past the end
+    multiply(cur, cur + TA::kBytes, wm, wn, lane, acc);
+    store(tid, nxt, nxt + TA::kBytes, ra, rb);
+    __syncthreads();
+  }
+  // All whole steps through a ring of kStages steps in the LDS: kStages - 1 are
+  // on their way or there while one is multiplied. A tile of few waves has
+  // nothing else to cover the loads' latency with.
+  __device__ static __forceinline__ void ring(const Where& t, int steps, int tid, int wave, const uint32_t* oa,
+                                              const uint32_t* ob, char* s, int wm, int wn, int lane, v4f (*acc)[kMF]) {
+    int to = 0;  // bytes: the stage that is loaded next
+    const auto next = [](int at) { return at == (kStages - 1) * kStage ? 0 : at + kStage; };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i, to = next(to))
+      if (i < steps) fetch(t, i * kK, tid, wave, oa, ob, s + to);
+    int at = 0;
+    for (int i = 0; i < steps; ++i, at = next(at)) {
+      // step i has landed, in every wave, and step i - 1 has been read
+      if (i + kStages - 2 < steps) meet<(kStages - 2) * (kPA + kPB)>();
+      else meet<0>();
+      if (i + kStages - 1 < steps) fetch(t, (i + kStages - 1) * kK, tid, wave, oa, ob, s + to);
+      to = next(to);
+      multiply(s + at, s + at + TA::kBytes, wm, wn, lane, acc);
     }
+    meet<0>();
   }
   // Two groups of four waves, one wave of each per SIMD, a phase apart: while
   // one reads its fragments of a half step from the LDS the other multiplies,
@@ -358,91 +530,58 @@ struct Gemm {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Own loads have landed and own reads are done, in every wave.
+  // Own loads but the last LATER have landed and own reads are done, in every wave.
+  template <int LATER = 0>
   __device__ static __forceinline__ void meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LATER) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
 };
 
-template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+// One tile. (A 256 x 256 tile's workgroup has its compute unit to itself; one
+// that took tile after tile, the next one's first step loading during the
+// epilogue, was slower: 302 us beside 275 for 8192 x 4096 x 4096, 259 beside
+// 249 for the experts' 32768 rows, since a tile then waits for the stores of
+// the one before.)
+template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmArgs a) {
-  using G = Gemm<DT, MODE, GATED, DIRECT, BM, BN, WM, WN>;
-  constexpr int kES = G::kES, kK = G::kK, kMF = G::kMF, kNF = G::kNF;
-  __shared__ __align__(16) char s0[G::TA::kBytes + G::TB::kBytes];
-  __shared__ __align__(16) char s1[G::TA::kBytes + G::TB::kBytes];
+  using G = Gemm<DT, MODE, GATED, DIRECT, BM, BN, WM, WN, STAGES>;
+  constexpr int kK = G::kK, kMF = G::kMF, kNF = G::kNF;
+  __shared__ __align__(16) char s0[G::kStages * G::kStage];
+  char* s1 = s0 + G::kStage;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave % (BM / WM)) * WM, wn = (wave / (BM / WM)) * WN;
-
-  // the tile: rank, group, rows and columns
-  int b = xcd_order(blockIdx.x, gridDim.x);
-  const int nti = b % a.nt;
-  b /= a.nt;
-  int r, g, row0;
-  typename G::Where t;
-  if constexpr (MODE == kDw) {
-    const int mti = b % a.mt;
-    b /= a.mt;
-    g = b % a.G;
-    r = b / a.G;
-    const GroupTile q = find_group<true>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, 1, g, a.err);
-    row0 = q.first;
-    t.K = q.count;
-    t.m0 = mti * BM;
-    t.mEnd = a.M;
-  } else {
-    const int slot = b % a.mt;
-    r = b / a.mt;
-    const GroupTile q = find_group<false>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
-    if (q.g < 0) return;
-    g = q.g;
-    row0 = q.first;
-    t.K = a.K;
-    t.m0 = (slot - q.tile0) * BM;
-    t.mEnd = q.count;
-  }
-  t.n0 = nti * BN;  // tile's first column of b; gated: BN / 2 columns of either half
-  t.N = a.N;
-  t.O = a.O;
-  t.lda = a.lda * kES;
-  t.ldb = a.ldb * kES;
-  t.width_a = static_cast<int>(a.lda);
-  t.width_b = static_cast<int>(a.ldb);
-  t.pa = a.a.p[r] + (uint64_t)row0 * t.lda + (MODE != kDw ? (uint64_t)t.m0 * t.lda : 0);
-  t.pb = a.b.p[r] + (MODE == kDw ? (uint64_t)row0 * t.ldb : (uint64_t)g * a.b_group * kES) +
-         (MODE == kFwd ? (uint64_t)(GATED ? t.n0 / 2 : t.n0) * t.ldb : 0);
+  typename G::Spot at;
+  if (!G::locate(a, xcd_order(blockIdx.x, gridDim.x), &at)) return;
+  const typename G::Where& t = at.t;
 
   v4f acc[kNF][kMF];
 #pragma unroll
   for (int i = 0; i < kNF; ++i)
 #pragma unroll
     for (int j = 0; j < kMF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-
-  uint32_t oa[G::kPA], ob[G::kPB];
-  // whole steps (DIRECT; the others zero-fill and take every step here), two at a time
+  // whole steps (DIRECT; the others zero-fill and take every step here)
   const int steps = DIRECT ? t.K / kK : (t.K + kK - 1) / kK;
   if (steps > 0) {
     if constexpr (DIRECT) {
+      uint32_t oa[G::kPA], ob[G::kPB];
       G::offsets(t, tid, oa, ob);
-      G::fetch(t, 0, tid, wave, oa, ob, s0);
-      G::meet();
+      if constexpr (G::kThreads == 512) {
+        G::fetch(t, 0, tid, wave, oa, ob, s0);
+        G::meet();
+        if (wave < 4) G::template phases<true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+        else G::template phases<false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+      } else {
+        G::ring(t, steps, tid, wave, oa, ob, s0, wm, wn, lane, acc);
+      }
     } else {
       v4u ra[G::kPA], rb[G::kPB];
       G::load(t, tid, 0, ra, rb);
       G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
       __syncthreads();
-    }
-    if constexpr (DIRECT && G::kThreads == 512) {
-      if (wave < 4) G::template phases<true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
-      else G::template phases<false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
-    } else {
-    int i = 0;
-    for (; i + 2 <= steps; i += 2) {
-      G::step(t, (i + 1) * kK, true, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
-      G::step(t, (i + 2) * kK, i + 2 < steps, tid, wave, oa, ob, s1, s0, wm, wn, lane, acc);
-    }
-    if (i < steps) G::step(t, t.K, false, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+      for (int i = 0; i < steps; ++i)
+        G::step(t, (i + 1) * kK, tid, (i & 1) ? s1 : s0, (i & 1) ? s0 : s1, wm, wn, lane, acc);
     }
   }
   if (DIRECT && steps * kK < t.K) {  // the last, partial step: by registers, zero-filled
@@ -452,27 +591,65 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
     __syncthreads();
     G::multiply(s0, s0 + G::TA::kBytes, wm, wn, lane, acc);
   }
+  G::template finish<ACT>(a, at, wm, wn, lane, acc);
+}
 
-  const int cq = (lane >> 4) * 4;
+// Few rows (MT * 16 at a time) against many weights: bound by the weights'
+// bytes. A workgroup takes 16 columns of out (gated: 16 of either half), its 8
+// waves an eighth of the contraction axis each; weights and rows go straight
+// to registers, and the waves' sums meet in the LDS once, at the end. One row of
+// 4096 x 4096 bf16 weights: 128-column tiles, of which there are only 32, took
+// 45 us.
+template <int DT, int ACT, bool GATED, int MT>
+__global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
+  constexpr int kES = Elem<DT>::kSize, kStep = 4 * Elem<DT>::kChunk, NW = GATED ? 2 : 1, BM = MT * 16;
+  constexpr int U = 16 / (NW + MT);  // 64 registers of loads in flight
+  __shared__ __align__(16) v4f part[8][NW][BM][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+  int b = blockIdx.x;
+  const int slot = b % a.mt;
+  b /= a.mt;
+  const int c0 = b % a.nt * 16, r = b / a.nt;
+  const GroupTile g = find_group<false>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
+  if (g.g < 0) return;
+  const int m0 = (slot - g.tile0) * BM, rows = min(g.count - m0, BM), first = g.first + m0;
+  const char *w[NW], *x[MT];
+  const int col = min(c0 + i, a.O - 1);
 #pragma unroll
-  for (int j = 0; j < kMF; ++j) {
-    const int m = t.m0 + wm + j * 16 + (lane & 15);
-    if (m >= t.mEnd) continue;
+  for (int h = 0; h < NW; ++h) w[h] = a.b.p[r] + ((uint64_t)g.g * a.b_group + (uint64_t)(h * a.O + col) * a.ldb) * kES;
 #pragma unroll
-    for (int i = 0; i < kNF; i += GATED ? 2 : 1) {
-      if constexpr (MODE == kFwd) {
-        const int col = GATED ? t.n0 / 2 + (wn + i * 16) / 2 + cq : t.n0 + wn + i * 16 + cq;
-        epilogue<DT, ACT, GATED>(a, r, g, row0 + m, col, acc[i][j], acc[i + (GATED ? 1 : 0)][j]);
-      } else {
-        const int col = t.n0 + wn + i * 16 + cq;
-        float y[4];
+  for (int j = 0; j < MT; ++j) x[j] = a.a.p[r] + (uint64_t)(first + min(j * 16 + i, rows - 1)) * a.lda * kES;
+  v4f z[NW][MT];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] = acc[i][j][q];
-        const uint64_t row = MODE == kDw ? (uint64_t)m : (uint64_t)(row0 + m);
-        if (col < a.N) store4<DT>(a.out.p[r] + (uint64_t)g * a.out_group * kES, row * a.N + col, a.N - col, y);
-      }
-    }
-  }
+  for (int h = 0; h < NW; ++h)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) z[h][j] = v4f{0, 0, 0, 0};
+  const int per = (a.K + 8 * kStep - 1) / (8 * kStep) * kStep;
+  stream_products<DT, NW, MT, U>(w, x, wave * per, min(a.K, (wave + 1) * per), a.K, z);
+#pragma unroll
+  for (int h = 0; h < NW; ++h)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[wave][h][j * 16 + i][q] = z[h][j];
+  __syncthreads();
+  const int m = tid >> 2, p = tid & 3;
+  if (m >= rows) return;
+  v4f s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+  for (int h = 0; h < NW; ++h)
+#pragma unroll
+    for (int v = 0; v < 8; ++v) s[h] += part[v][h][m][p];
+  epilogue<DT, ACT, GATED>(a, r, g.g, first + m, c0 + p * 4, s[0], s[1]);
+}
+
+template <int DT, int ACT, bool GATED, int MT>
+vrResult_t launch_few(GemmArgs& a, hipStream_t st) {
+  a.mt = a.counts ? a.rows / (MT * 16) + a.G : (a.rows + MT * 16 - 1) / (MT * 16);
+  a.nt = (a.O + 15) / 16;
+  const uint64_t grid = (uint64_t)a.R * a.mt * a.nt;
+  if (!grid) return VR_OK;
+  if (grid > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
+  hipLaunchKernelGGL((k_few<DT, ACT, GATED, MT>), dim3(static_cast<uint32_t>(grid)), dim3(512), 0, st, a);
+  return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
 
 // Whether every row of the present parts of both operands starts on 16 bytes.
@@ -482,7 +659,7 @@ bool rows_aligned(const GemmArgs& a, int es) {
   return v % 16 == 0;
 }
 
-template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN>
+template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   if (MODE == kDw) a.mt = (a.M + BM - 1) / BM;
   else a.mt = a.counts ? a.rows / BM + a.G : (a.rows + BM - 1) / BM;
@@ -490,20 +667,39 @@ vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   const uint64_t grid = (uint64_t)a.R * (MODE == kDw ? a.G : 1) * a.mt * a.nt;
   if (!grid) return VR_OK;
   if (grid > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
-  hipLaunchKernelGGL((k_gemm<DT, MODE, ACT, GATED, DIRECT, BM, BN, WM, WN>), dim3(static_cast<uint32_t>(grid)),
+  hipLaunchKernelGGL((k_gemm<DT, MODE, ACT, GATED, DIRECT, BM, BN, WM, WN, STAGES>), dim3(static_cast<uint32_t>(grid)),
                      dim3(64 * (BM / WM) * (BN / WN)), 0, st, a);
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
 
+// The tile: the largest that leaves no compute unit without one. bf16 4096 x
+// 4096 weights, us at 128, 512, 1024, 2048 rows: 64 x 64 tiles with two steps
+// in the LDS 34, 42, 62, 129, with three 23, 42, 79, 153; 128 x 128 tiles 50,
+// 52, 56, 74; 256 x 256 tiles 110, 115, 115, 118 and at 8192 rows a quarter
+// less than 128 x 128.
+template <int DT, int MODE, int ACT, bool GATED, bool DIRECT>
+vrResult_t launch_any(GemmArgs& a, hipStream_t st) {
+  const uint64_t m = MODE == kDw ? (uint64_t)a.M * a.G : (uint64_t)a.rows, size = (uint64_t)a.R * m * a.N;
+  if constexpr (DT == VR_DT_BF16 && DIRECT) {
+    if (size >= 200ull * 256 * 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
+  }
+  if (size >= 256ull * 128 * 128) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
+  if (DIRECT && size <= 512ull * 64 * 64) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 3>(a, st);
+  return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 2>(a, st);
+}
+
 template <int DT, int MODE, int ACT, bool GATED>
 vrResult_t launch_gemm(GemmArgs& a, hipStream_t st) {
-  if (!rows_aligned(a, Elem<DT>::kSize)) return launch_tiles<DT, MODE, ACT, GATED, false, 128, 128, 64, 64>(a, st);
-  if constexpr (DT == VR_DT_BF16) {
-    // 256 x 256 tiles once they fill the chip
-    const uint64_t m = MODE == kDw ? (uint64_t)a.M * a.G : (uint64_t)a.rows;
-    if ((uint64_t)a.R * m * a.N >= 200ull * 256 * 256) return launch_tiles<DT, MODE, ACT, GATED, true, 256, 256, 128, 64>(a, st);
+  if constexpr (MODE == kFwd) {
+    // Few rows: against 64 x 64 tiles, us at 1, 32, 64 rows of bf16 4096 x 4096
+    // weights 11, 15, 25 to 22; at 64, 256 rows of fp32 2048 x 2048 weights, whose
+    // tiles are bound by the matrix units, 16, 47 to 45. Groups are ragged.
+    const int most = (DT == VR_DT_F32 ? 128 : 32) / (a.G > 1 ? 2 : 1), rows = a.rows / a.G;
+    if (rows <= 16 && rows <= most) return launch_few<DT, ACT, GATED, 1>(a, st);
+    if (rows <= most) return launch_few<DT, ACT, GATED, 2>(a, st);
   }
-  return launch_tiles<DT, MODE, ACT, GATED, true, 128, 128, 64, 64>(a, st);
+  return rows_aligned(a, Elem<DT>::kSize) ? launch_any<DT, MODE, ACT, GATED, true>(a, st)
+                                          : launch_any<DT, MODE, ACT, GATED, false>(a, st);
 }
 
 // ---- the gradient of z, and of the bias ---------------------------------------------------
