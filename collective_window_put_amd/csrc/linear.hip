@@ -672,19 +672,32 @@ vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
 
-// The tile: the largest that leaves no compute unit without one. bf16 4096 x
-// 4096 weights, us at 128, 512, 1024, 2048 rows: 64 x 64 tiles with two steps
-// in the LDS 34, 42, 62, 129, with three 23, 42, 79, 153; 128 x 128 tiles 50,
-// 52, 56, 74; 256 x 256 tiles 110, 115, 115, 118 and at 8192 rows a quarter
-// less than 128 x 128.
+// Tiles of size n x n to expect: a group's last row tile is half empty.
+template <int MODE, bool GATED>
+uint64_t expected_tiles(const GemmArgs& a, int n) {
+  const uint64_t cols = GATED ? (a.O + n / 2 - 1) / (n / 2) : (a.N + n - 1) / n;
+  if (MODE == kDw) return (uint64_t)a.R * a.G * ((a.M + n - 1) / n) * cols;
+  return a.R * (a.counts ? (uint64_t)a.rows / n + (a.G + 1) / 2 : (a.rows + n - 1) / n) * cols;
+}
+
+// The tile. 256 x 256 tiles take a compute unit each, 128 x 128 tiles share
+// one by two; a round of the latter, half the products, takes 0.59 of a round
+// of the former (81 and 137 us of 8192 x 4096 x 4096 bf16), and whichever
+// needs the less time in whole rounds is taken. 128 x 128 tiles need to give
+// every compute unit one; below that, bf16 4096 x 4096 weights take at 128,
+// 512, 1024 rows: 64 x 64 tiles with two steps in the LDS 34, 42, 62 us, with
+// three 23, 42, 79; 128 x 128 tiles 50, 52, 56.
 template <int DT, int MODE, int ACT, bool GATED, bool DIRECT>
 vrResult_t launch_any(GemmArgs& a, hipStream_t st) {
-  const uint64_t m = MODE == kDw ? (uint64_t)a.M * a.G : (uint64_t)a.rows, size = (uint64_t)a.R * m * a.N;
+  const uint64_t n128 = expected_tiles<MODE, GATED>(a, 128);
   if constexpr (DT == VR_DT_BF16 && DIRECT) {
-    if (size >= 200ull * 256 * 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
+    const uint64_t n256 = expected_tiles<MODE, GATED>(a, 256);
+    if ((n256 + 255) / 256 * 100 <= (n128 + 511) / 512 * 59)
+      return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
   }
-  if (size >= 256ull * 128 * 128) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
-  if (DIRECT && size <= 512ull * 64 * 64) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 3>(a, st);
+  if (n128 >= 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
+  if (DIRECT && expected_tiles<MODE, GATED>(a, 64) <= 512)
+    return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 3>(a, st);
   return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 2>(a, st);
 }
 
