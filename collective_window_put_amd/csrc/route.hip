@@ -334,10 +334,13 @@ __global__ __launch_bounds__(kThreads) void k_route_backward_rows(const RouteArg
   const int rank = blockIdx.y, t0 = blockIdx.x * kWaves * 4 + row, t = min(t0, a.T - 1);
   const uint64_t from = (uint64_t)t * a.E * Elem<DT>::kSize;
   float p[V];
-  if (!a.renorm) load_row<DT, V>(a.logits.p[rank] + from, a.E, s, p);
+  // rows past the last token load nothing: dlogits may be the logits, already overwritten
+#pragma unroll
+  for (int j = 0; j < V; ++j) p[j] = -INFINITY;
+  if (!a.renorm && t0 < a.T) load_row<DT, V>(a.logits.p[rank] + from, a.E, s, p);
   int e = -1;
   float w = 0.0f, dw = 0.0f;
-  if (s < a.K) {
+  if (s < a.K && t0 < a.T) {
     const uint64_t at = ((uint64_t)rank * a.T + t) * a.K + s;
     e = a.topk_in[at];
     w = a.weights_in[at];
