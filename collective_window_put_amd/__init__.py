@@ -264,7 +264,10 @@ def _ptr(x) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if not torch.cuda.is_initialized():
+            return int(torch.cuda.current_stream().cuda_stream)
+        # the same stream without a Stream object, which takes 3 us to make: most of a small call's time on the host
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
