@@ -33,8 +33,10 @@ struct GemmArgs {
 //   KC (the contraction axis is contiguous): piece c of row r at position
 //      c ^ (r & 7) of the row's 128 bytes, so that the 16 rows of a fragment
 //      read fall on all banks;
-//   otherwise rows of ROWS columns per k; pieces are exchanged so that the 4
-//      rows (bf16) or the 4 row quarters (fp32) of one read do.
+//   otherwise rows of ROWS columns per k; pieces are exchanged so that the
+//      rows of one read do: bf16, 4 rows for each 16 lanes, and the 4 rows 8
+//      further on for the next 16 (with the first 4 alone, half the LDS's
+//      cycles in dw were conflicts); fp32, the 4 row quarters.
 template <int DT, bool KC, int ROWS>
 struct Tile {
   static constexpr int kK = 128 / Elem<DT>::kSize;       // contraction elements
@@ -44,7 +46,7 @@ struct Tile {
   static constexpr int kPerRow = KC ? 8 : ROWS / kC;     // pieces per stored row
   __device__ static int swz(int r) {
     if constexpr (KC) return r & 7;
-    else if constexpr (DT == VR_DT_BF16) return (r & 3) << 1;
+    else if constexpr (DT == VR_DT_BF16) return ((r & 3) | (ROWS >= 128 ? (r >> 1) & 4 : 0)) << 1;
     else return ((r >> 2) & 3) << 2;
   }
   // Fragment of 16 rows (columns) from `base`, pieces ks: lane l holds
@@ -268,14 +270,18 @@ struct Gemm {
     Where t;
     int r, g, row0;
   };
-  // Tile b of the launch: column tiles, then row tiles, then groups (kDw) and
+  // Tile b of the launch: tiles of a group (kDw) or rank, then groups and
   // ranks. False when there is no such tile.
   __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s) {
     Where& t = s->t;
-    const int nti = b % a.nt;
-    b /= a.nt;
-    const int slot = b % a.mt;
-    b /= a.mt;
+    int nti = b % a.nt, slot = b / a.nt % a.mt;
+    b /= a.nt * a.mt;
+    if (MODE == kDw || !a.counts) {
+      // a band of 8 row tiles, column by column: the tiles that run on one XCD at a time are 8 by 4
+      const int band = slot / 8 * 8, high = min(8, a.mt - band), in = (slot - band) * a.nt + nti;
+      slot = band + in % high;
+      nti = in / high;
+    }
     if constexpr (MODE == kDw) {
       s->g = b % a.G;
       s->r = b / a.G;

@@ -178,8 +178,8 @@ inline void with_act(uint32_t act, F f) {
 
 // ---- wave reductions ------------------------------------------------------------------
 // Lane l's partner in step S of a reduction, over vector instructions alone
-// (no trip through the LDS: six steps of a maximum took 0.5 us that way, and
-// take 0.05 us this way): lanes 1 and 2 apart, then mirrored in 8 and in 16
+// (a shuffle is a trip through the LDS, and the router waits for each): lanes
+// 1 and 2 apart, then mirrored in 8 and in 16
 // lanes (by then 4 and 8 lanes hold equal values), then rows 16 and 32 apart.
 // The two values of a step are the same in both partners, so every lane gets
 // the same result, bit for bit.
