@@ -225,7 +225,8 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 // (`to` the same in all lanes). In asm so that the compiler, which cannot tell
 // the two halves of the LDS apart across a loop, does not wait for it before
 // every LDS read: the caller waits for vmcnt and meets at a barrier instead.
-// There is no output register, and the address is read when it issues.
+// There is no output register, and the address is read when it issues. m0 is
+// reserved: the compiler keeps nothing in it between instructions.
 __device__ inline void load_lds16(const char* base, uint32_t off, char* to) {
   const uint32_t lds = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to)));
@@ -702,8 +703,10 @@ vrResult_t launch_any(GemmArgs& a, hipStream_t st) {
       return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
   }
   if (n128 >= 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
-  if (DIRECT && expected_tiles<MODE, GATED>(a, 64) <= 512)
-    return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 3>(a, st);
+  if constexpr (DIRECT) {
+    if (expected_tiles<MODE, GATED>(a, 64) <= 512)
+      return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 3>(a, st);
+  }
   return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 64, 32, 32, 2>(a, st);
 }
 
