@@ -739,7 +739,10 @@ struct DzArgs {
 };
 
 // A workgroup takes kDzRows rows of one group and 64 * V columns; its four
-// waves take every fourth row.
+// waves take every fourth row, kAhead rows' loads in flight (64 rows of 4096
+// columns, few workgroups: 13.8 us a row at a time, 10.0
+// this way).
+constexpr int kAhead = 4;
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void k_dz(const DzArgs a) {
   constexpr int V = Elem<DT>::kChunk;
@@ -752,54 +755,61 @@ __global__ __launch_bounds__(256) void k_dz(const DzArgs a) {
   float sg[V], su[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) sg[j] = su[j] = 0.0f;
-  for (int i = first + wave; i < last && n > 0; i += 4) {
-    const uint64_t row = t.first + i;
-    float d[V], g[V], u[V];
-    auto get = [&](const char* base, uint64_t at, float* f) {
-      if (n >= V) {
-        load_n<DT, V>(base, at, f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = j < n ? Elem<DT>::load(base, at + j) : 0.0f;
-      }
-    };
-    auto put = [&](uint64_t at, const float* f) {
-      char* base = a.dz + (uint64_t)r * a.dz_rank;
-      if (n >= V) {
-        store_n<DT, V>(base, at, f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j < n) Elem<DT>::store(base, at + j, f[j]);
-      }
-    };
-    get(a.dout.p[r], row * a.O + col, d);
-    if (a.preact.p[r]) {
-      get(a.preact.p[r], row * a.N + col, g);
-      if (GATED) get(a.preact.p[r], row * a.N + a.O + col, u);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float y, s;
-        act_both<DT>(g[j], a.act, &y, &s);
-        if (GATED) {
-          g[j] = d[j] * u[j] * s;
-          u[j] = d[j] * y;
-        } else {
-          g[j] = d[j] * s;
-        }
-      }
+  const bool whole = (blockIdx.y + 1) * 64 * V <= static_cast<uint32_t>(a.O);  // the same in all lanes: no branch at a load
+  const auto get = [&](const char* base, uint64_t at) {
+    const char* q = base + at * Elem<DT>::kSize;
+    return whole ? load_whole<DT>(q) : load_piece<DT>(q, n);
+  };
+  const auto put = [&](uint64_t at, const float* f) {
+    char* base = a.dz + (uint64_t)r * a.dz_rank;
+    if (n >= V) {
+      store_n<DT, V>(base, at, f);
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) g[j] = d[j];
+      for (int j = 0; j < V; ++j)
+        if (j < n) Elem<DT>::store(base, at + j, f[j]);
     }
-    if (a.dz) {
-      put(row * a.ldz + col, g);
-      if (GATED) put(row * a.ldz + a.O + col, u);
+  };
+  for (int i0 = first + wave; i0 < last && n > 0; i0 += 4 * kAhead) {
+    v4u dv[kAhead], gv[kAhead], uv[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint64_t row = t.first + min(i0 + 4 * k, last - 1);
+      dv[k] = get(a.dout.p[r], row * a.O + col);
+      if (a.preact.p[r]) {
+        gv[k] = get(a.preact.p[r], row * a.N + col);
+        if (GATED) uv[k] = get(a.preact.p[r], row * a.N + a.O + col);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      sg[j] += g[j];
-      if (GATED) su[j] += u[j];
+    for (int k = 0; k < kAhead; ++k) {
+      if (i0 + 4 * k >= last) break;
+      const uint64_t row = t.first + i0 + 4 * k;
+      float g[V], u[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float d = piece_f32<DT>(dv[k], j);
+        g[j] = d;
+        if (a.preact.p[r]) {
+          float y, slope;
+          act_both<DT>(piece_f32<DT>(gv[k], j), a.act, &y, &slope);
+          if (GATED) {
+            g[j] = d * piece_f32<DT>(uv[k], j) * slope;
+            u[j] = d * y;
+          } else {
+            g[j] = d * slope;
+          }
+        }
+      }
+      if (a.dz) {
+        put(row * a.ldz + col, g);
+        if (GATED) put(row * a.ldz + a.O + col, u);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sg[j] += g[j];
+        if (GATED) su[j] += u[j];
+      }
     }
   }
   if (!a.partial) return;
@@ -817,18 +827,23 @@ __global__ __launch_bounds__(256) void k_dz(const DzArgs a) {
   }
 }
 
-// dbias[g][n]: the group's row tiles in order.
+// dbias[g][n] of 64 columns: four waves sum a quarter of the group's row tiles
+// each, in order. (A thread for a whole column, 4096 columns and 128 tiles:
+// 7.5 us, bound by the loads' latency; this way about 5.)
 template <int DT>
 __global__ __launch_bounds__(256) void k_dbias(const DzArgs a) {
-  const int r = blockIdx.z, g = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  const int r = blockIdx.z, g = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * 64 + lane;
   const GroupTile t = find_group<true>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, kDzRows, g, a.err);
-  if (n >= a.N) return;
-  const int tiles = (t.count + kDzRows - 1) / kDzRows;
-  const float* p = a.partial + ((uint64_t)r * a.slots + t.tile0) * a.N + n;
+  const int tiles = (t.count + kDzRows - 1) / kDzRows, per = (tiles + 3) / 4, last = min(tiles, (wave + 1) * per);
+  const float* p = a.partial + ((uint64_t)r * a.slots + t.tile0) * a.N + min(n, a.N - 1);
   float s = 0.0f;
 #pragma unroll 8
-  for (int i = 0; i < tiles; ++i) s += p[(uint64_t)i * a.N];
-  Elem<DT>::store(a.dbias.p[r], (uint64_t)g * a.N + n, s);
+  for (int i = wave * per; i < last; ++i) s += p[(uint64_t)i * a.N];
+  __shared__ float part[4][64];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave || n >= a.N) return;
+  Elem<DT>::store(a.dbias.p[r], (uint64_t)g * a.N + n, (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
 }
 
 bool gated(const vrLinearShape& s) { return (s.act & VR_ACT_GATED) != 0; }
@@ -910,7 +925,7 @@ vrResult_t linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dou
     if (gated(s)) hipLaunchKernelGGL((k_dz<DT, true>), grid, dim3(256), 0, st, z);
     else hipLaunchKernelGGL((k_dz<DT, false>), grid, dim3(256), 0, st, z);
   }
-  if (z.partial) hipLaunchKernelGGL((k_dbias<DT>), dim3((N + 255) / 256, s.groups, R), dim3(256), 0, st, z);
+  if (z.partial) hipLaunchKernelGGL((k_dbias<DT>), dim3((N + 63) / 64, s.groups, R), dim3(256), 0, st, z);
   if (hipGetLastError() != hipSuccess) return VR_ERR_HIP;
 
   GemmArgs a = {};

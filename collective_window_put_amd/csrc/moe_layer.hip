@@ -41,11 +41,6 @@ struct MoeArgs {
   uint32_t act;
 };
 
-template <int DT>
-__device__ inline float piece_f32(v4u v, int j) {
-  if constexpr (DT == VR_DT_F32) return __uint_as_float(v[j]);
-  else return (j & 1) ? bf16hi(v[j / 2]) : bf16lo(v[j / 2]);
-}
 // A token's logits of experts e0 .. e0 + 3 into out[0 .. 3], by one wave.
 // Products of two elements are exact in binary64; the choice of the K largest
 // is then that of the exact logits except within a few 2^-53.

@@ -328,6 +328,13 @@ __device__ inline v4u load_piece(const char* p, int n) {
   return v;
 }
 
+// Element j of a piece.
+template <int DT>
+__device__ inline float piece_f32(v4u v, int j) {
+  if constexpr (DT == VR_DT_F32) return __uint_as_float(v[j]);
+  else return (j & 1) ? bf16hi(v[j / 2]) : bf16lo(v[j / 2]);
+}
+
 // ---- matrix instructions -----------------------------------------------------------------
 // acc[i][j] += sum_k a[i][k] b[j][k] over one 16-byte piece per lane: lane l
 // holds elements k = (l / 16) * piece ... of row i = l % 16 of a and j = l % 16
