@@ -226,14 +226,18 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 // the two halves of the LDS apart across a loop, does not wait for it before
 // every LDS read: the caller waits for vmcnt and meets at a barrier instead.
 // There is no output register, and the address is read when it issues. m0 is
-// reserved: the compiler keeps nothing in it between instructions.
+// reserved: the compiler keeps nothing in it between instructions. Five wait
+// states have to lie between a vector instruction that writes a scalar
+// register (v_readfirstlane, or v_readlane of a spilled one) and a vector memory
+// instruction that reads it; the compiler keeps this in its own code but does
+// not look into asm, so all five are here: s_mov and s_nop 3.
 __device__ inline void load_lds16(const char* base, uint32_t off, char* to) {
   const uint32_t lds = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to)));
   const uint64_t at = reinterpret_cast<uintptr_t>(base);
   const uint64_t uniform = (static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32))) << 32) |
                            static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform) : "memory");
 }
 
