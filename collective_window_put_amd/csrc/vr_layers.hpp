@@ -95,8 +95,14 @@ __device__ inline float sigmoid(float z) {
 template <int DT>
 __device__ inline float normal_cdf(float z, float* e) {
   if constexpr (DT == VR_DT_F32) {
+    // erfc multiplies its argument's relative error by z^2: the argument's two
+    // roundings (of 1 / sqrt 2 and of the product) are put back to first order,
+    // d erfc(t) = -2 / sqrt(pi) exp(-t^2) dt with exp(-t^2) = *e. At z = -11.6
+    // they took 1e-5 of the value.
     *e = expf(-0.5f * z * z);
-    return 0.5f * erfcf(z * -0.70710678118654752f);
+    const float t = z * -0.70710678f;
+    const float off = fmaf(z, -0.70710678f, -t) + z * -1.2101617e-8f;
+    return 0.5f * erfcf(t) - (fabsf(z) < 16.0f ? off * *e * 0.56418958f : 0.0f);
   } else {
     *e = fast_exp(-0.5f * z * z);
     const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
