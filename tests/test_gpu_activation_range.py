@@ -63,7 +63,7 @@ def _run(job, z, rows, act, gated, dtype, I=8):  # noqa: E741
 
 @pytest.mark.parametrize("rows,gated", [(1, False), (1, True), (200, False), (70, True)])
 @pytest.mark.parametrize("act", ["gelu", "silu"])
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_whole_range(dtype, act, rows, gated):
     say(f"activation range: {dtype} {act} rows={rows} gated={gated}")
     z = np.unique(round_to(np.concatenate([np.linspace(-12.0, 12.0, 1501), [-2.0 ** -40, 0.0, 2.0 ** -40, -0.7518, -1.2785]]), dtype))
@@ -81,8 +81,33 @@ def test_whole_range(dtype, act, rows, gated):
         job.assert_no_async_error()
 
 
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_few_token_layer_over_the_range(act):
+    # x is the first unit vector, so w_up's first column is the argument; w_down is the identity, one expert of weight 1
+    import torch
+    say(f"activation range: few-token layer {act}")
+    z = round_to(np.linspace(-12.0, 12.0, 512), "bf16")
+    n = z.size
+    for T in (1, 3):
+        x, up = np.zeros((1, T, n)), np.zeros((1, 1, n, n))
+        x[..., 0], up[0, 0, :, 0] = 1.0, z
+        shape = vr.vrMoeShape(vr.VR_DT_BF16, T, n, n, 1, 1, ACT[act], vr.VR_ROUTE_RENORM)
+        need = vr.vr_moe_layer_workspace_bytes(1, shape)
+        with Job(1) as job:
+            tn = Tensors(job, "bf16")
+            out, read = tn.put(shape=(T, n), fill=5.0)
+            idx = torch.zeros((1, T, 1), dtype=torch.int32, device="cuda")
+            w = torch.zeros((1, T, 1), device="cuda")
+            vr.vr_moe_layer(job.comm, shape, tn.put(x)[0], torch.zeros(1, n, device="cuda").bfloat16(), tn.put(up)[0],
+                            tn.put(np.eye(n).reshape(1, 1, n, n))[0], out, idx, w, workspace=workspace(need), workspace_bytes=need)
+            y, _ = definition(z, act)
+            for t in range(T):  # 2^-16: held as two bf16 parts
+                check(read()[0, t], y, np.abs(y) * (relative(z, act, "bf16") + 2.0 ** -16), f"token {t} of {T}")
+            job.assert_no_async_error()
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_infinities_and_nan_as_in_the_definition(dtype, act):
     # z cdf(z) and z / (1 + exp(-z)) at -inf are -inf * 0, NaN, in both types
     say(f"activation of infinities: {dtype} {act}")
