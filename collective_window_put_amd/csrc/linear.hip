@@ -25,6 +25,7 @@ struct GemmArgs {
   uint64_t lda, ldb;      // elements
   uint64_t b_group, out_group;
   int mt, nt;             // row tiles per rank (kDw: per group), column tiles
+  int tile0;              // the launch's first tile
   uint32_t act;
 };
 
@@ -275,7 +276,7 @@ struct Gemm {
     Where t;
     int r, g, row0;
   };
-  // Tile b of the launch: tiles of a group (kDw) or rank, then groups and
+  // Tile b: tiles of a group (kDw) or rank, then groups and
   // ranks. False when there is no such tile.
   __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s) {
     Where& t = s->t;
@@ -564,7 +565,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave % (BM / WM)) * WM, wn = (wave / (BM / WM)) * WN;
   typename G::Spot at;
-  if (!G::locate(a, xcd_order(blockIdx.x, gridDim.x), &at)) return;
+  if (!G::locate(a, a.tile0 + xcd_order(blockIdx.x, gridDim.x), &at)) return;
   const typename G::Where& t = at.t;
 
   v4f acc[kNF][kMF];
@@ -617,7 +618,7 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
   constexpr int U = 16 / (NW + MT);  // 64 registers of loads in flight
   __shared__ __align__(16) v4f part[8][NW][BM][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
-  int b = blockIdx.x;
+  int b = a.tile0 + blockIdx.x;
   const int slot = b % a.mt;
   b /= a.mt;
   const int c0 = b % a.nt * 16, r = b / a.nt;
@@ -652,15 +653,27 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
   epilogue<DT, ACT, GATED>(a, r, g.g, first + m, c0 + p * 4, s[0], s[1]);
 }
 
+// A launch holds fewer than 2^32 threads in a direction; 2^22 workgroups of up to
+// 512 do. More tiles (a thousand groups of 128 thousand columns, say) take more
+// launches: launch(workgroups) with a.tile0 set, a multiple of 8 for xcd_order.
+template <class F>
+vrResult_t launch_parts(GemmArgs& a, uint64_t tiles, F launch) {
+  constexpr uint64_t kMost = 1u << 22;
+  if (tiles > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
+  for (uint64_t at = 0; at < tiles; at += kMost) {
+    a.tile0 = static_cast<int>(at);
+    launch(dim3(static_cast<uint32_t>(std::min(tiles - at, kMost))));
+  }
+  return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+}
+
 template <int DT, int ACT, bool GATED, int MT>
 vrResult_t launch_few(GemmArgs& a, hipStream_t st) {
   a.mt = a.counts ? a.rows / (MT * 16) + a.G : (a.rows + MT * 16 - 1) / (MT * 16);
   a.nt = (a.O + 15) / 16;
-  const uint64_t grid = (uint64_t)a.R * a.mt * a.nt;
-  if (!grid) return VR_OK;
-  if (grid > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
-  hipLaunchKernelGGL((k_few<DT, ACT, GATED, MT>), dim3(static_cast<uint32_t>(grid)), dim3(512), 0, st, a);
-  return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+  return launch_parts(a, (uint64_t)a.R * a.mt * a.nt, [&](dim3 grid) {
+    hipLaunchKernelGGL((k_few<DT, ACT, GATED, MT>), grid, dim3(512), 0, st, a);
+  });
 }
 
 // Whether every row of the present parts of both operands starts on 16 bytes.
@@ -675,12 +688,10 @@ vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   if (MODE == kDw) a.mt = (a.M + BM - 1) / BM;
   else a.mt = a.counts ? a.rows / BM + a.G : (a.rows + BM - 1) / BM;
   a.nt = GATED ? (a.O + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
-  const uint64_t grid = (uint64_t)a.R * (MODE == kDw ? a.G : 1) * a.mt * a.nt;
-  if (!grid) return VR_OK;
-  if (grid > 0x7FFFFFFFull) return VR_ERR_INVALID_ARGUMENT;
-  hipLaunchKernelGGL((k_gemm<DT, MODE, ACT, GATED, DIRECT, BM, BN, WM, WN, STAGES>), dim3(static_cast<uint32_t>(grid)),
-                     dim3(64 * (BM / WM) * (BN / WN)), 0, st, a);
-  return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+  return launch_parts(a, (uint64_t)a.R * (MODE == kDw ? a.G : 1) * a.mt * a.nt, [&](dim3 grid) {
+    hipLaunchKernelGGL((k_gemm<DT, MODE, ACT, GATED, DIRECT, BM, BN, WM, WN, STAGES>), grid,
+                       dim3(64 * (BM / WM) * (BN / WN)), 0, st, a);
+  });
 }
 
 // Tiles of size n x n to expect: a group's last row tile is half empty.

@@ -638,7 +638,8 @@ vrResult_t vr_route_backward(vrComm_t comm, vrSlice logits, int dtype, int T, in
  * VR_ACT_GATED the weights have N = 2 * out rows (the gate's, then the
  * linear half's), else N = out. groups: weight matrices per rank (local
  * experts), 1 for a dense layer; 1..1024. rows up to 2^24, in and out up to
- * 2^20. */
+ * 2^20; a product of 2^31 tiles or more over all ranks (at the smallest, a
+ * group's 16 rows by 16 columns) is refused. */
 typedef struct {
   int dtype;
   int rows;
