@@ -222,12 +222,11 @@ __global__ __launch_bounds__(512) void k_moe_up(const MoeArgs a) {
   __shared__ short ids[kMaxPairs], list[VR_MOE_LAYER_MAX_TOKENS];
   __shared__ uint32_t bits[32];
   __shared__ float part[8][NW][16][17];
-  const int cols = (a.I + 15) / 16;
   int e;
-  const int count = find_expert(a, blockIdx.x / cols, ids, bits, list, &e);
+  const int count = find_expert(a, blockIdx.y, ids, bits, list, &e);
   if (!count) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int c0 = blockIdx.x % cols * 16, epr = a.E / a.R;
+  const int c0 = blockIdx.x * 16, epr = a.E / a.R;
   const char* w = a.up.p[e / epr] + (uint64_t)(e % epr) * (GATED ? 2 : 1) * a.I * a.H * kES;
   const int col = min(c0 + i, a.I - 1);
   const char* wr[NW];
@@ -285,10 +284,9 @@ __global__ __launch_bounds__(512, 4) void k_moe_down(const MoeArgs a) {
   __shared__ short ids[kMaxPairs], list[VR_MOE_LAYER_MAX_TOKENS];
   __shared__ uint32_t bits[32];
   __shared__ float part[8][16][17];
-  const int cols = (a.H + CG * 16 - 1) / (CG * 16);
   int e;
-  const int count = find_expert(a, blockIdx.x / cols, ids, bits, list, &e);
-  const int cb = blockIdx.x % cols;
+  const int count = find_expert(a, blockIdx.y, ids, bits, list, &e);
+  const int cb = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
   const int c0 = (cb * CG + wave % CG) * 16, pt = wave / CG, epr = a.E / a.R;
   if (count) {
@@ -481,7 +479,8 @@ void launch_dt(const MoeArgs& a, hipStream_t st) {
   if (a.E <= 64) hipLaunchKernelGGL((k_moe_route<DT, 1>), dim3(a.N), dim3(threads), 0, st, a);
   else if (a.E <= 256) hipLaunchKernelGGL((k_moe_route<DT, 4>), dim3(a.N), dim3(threads), 0, st, a);
   else hipLaunchKernelGGL((k_moe_route<DT, 16>), dim3(a.N), dim3(threads), 0, st, a);
-  const dim3 up(slots * ((a.I + 15) / 16));
+  // columns, then experts, in a direction each: their product may pass the 2^32 threads that a direction holds
+  const dim3 up((a.I + 15) / 16, slots);
   with_act(a.act, [&](auto act) {
     if (a.act & VR_ACT_GATED) hipLaunchKernelGGL((k_moe_up<DT, act(), true>), up, dim3(512), 0, st, a);
     else hipLaunchKernelGGL((k_moe_up<DT, act(), false>), up, dim3(512), 0, st, a);
@@ -491,10 +490,11 @@ void launch_dt(const MoeArgs& a, hipStream_t st) {
     return;
   }
   // as many columns to a workgroup as leave the chip four of them per compute unit
-  const auto groups = [&](int cg) { return slots * ((a.H + cg * 16 - 1) / (cg * 16)); };
-  if (groups(8) >= 1024) hipLaunchKernelGGL((k_moe_down<DT, 8>), dim3(groups(8)), dim3(512), 0, st, a);
-  else if (groups(4) >= 512) hipLaunchKernelGGL((k_moe_down<DT, 4>), dim3(groups(4)), dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((k_moe_down<DT, 2>), dim3(groups(2)), dim3(512), 0, st, a);
+  const auto grid = [&](int cg) { return dim3((a.H + cg * 16 - 1) / (cg * 16), slots); };
+  const auto groups = [&](int cg) { return grid(cg).x * slots; };
+  if (groups(8) >= 1024) hipLaunchKernelGGL((k_moe_down<DT, 8>), grid(8), dim3(512), 0, st, a);
+  else if (groups(4) >= 512) hipLaunchKernelGGL((k_moe_down<DT, 4>), grid(4), dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((k_moe_down<DT, 2>), grid(2), dim3(512), 0, st, a);
   hipLaunchKernelGGL((k_moe_sum<DT>), dim3((a.H + 255) / 256, a.N), dim3(256), 0, st, a);
 }
 

@@ -90,3 +90,77 @@ def test_gradients_of_many_groups_and_inputs():
                 dw[r][g].zero_()
             assert not bool(dw[r].any()), r  # groups without rows
         job.assert_no_async_error()
+
+
+def _moe(job, T, E, K, H, I):
+    """Tensors of a few-token layer of relu experts, one rank, and a function that runs it."""
+    import torch
+    t = {k: _window(job, s) for k, s in dict(x=(T, H), up=(E, I, H), down=(E, H, I), out=(T, H)).items()}
+    router = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(1, T, K, dtype=torch.int32, device="cuda")
+    weights = torch.zeros(1, T, K, device="cuda")
+    shape = vr.vrMoeShape(vr.VR_DT_BF16, T, H, I, E, K, vr.VR_ACT_RELU, vr.VR_ROUTE_RENORM)
+    need = vr.vr_moe_layer_workspace_bytes(1, shape)
+    room = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def run():
+        vr.vr_moe_layer(job.comm, shape, t["x"][1], router, t["up"][1], t["down"][1], t["out"][1], idx, weights,
+                        workspace=room, workspace_bytes=need)
+        torch.cuda.synchronize()
+        job.assert_no_async_error()
+    return {k: v[0][0] for k, v in t.items()}, router, idx[0], weights[0], run
+
+
+def test_few_token_layer_of_many_experts_and_inner_columns():
+    # 1024 experts of 131104 inner columns: 8194 * 1024 workgroups of 512 threads for the up product
+    import torch
+    T, E, K, H, I = 64, 1024, 16, 6, 131104  # noqa: E741
+    assert E * (I // 16) * 512 > 1 << 32
+    say("moe layer: 1024 experts of 131104 inner columns")
+    with Job(1) as job:
+        t, router, idx, weights, run = _moe(job, T, E, K, H, I)
+        # token n is the signs of n's bits; experts n K .. n K + K - 1 look like it (logit 6, others 4 or less)
+        signs = (torch.arange(T, device="cuda")[:, None] >> torch.arange(H, device="cuda") & 1) * 2.0 - 1.0
+        t["x"].copy_(signs)
+        router.copy_(signs.repeat_interleave(K, 0))
+        for name, seed in (("up", 2), ("down", 3)):  # every column adds something positive to its token's sum
+            _normal(t[name], seed)
+            t[name].abs_()
+        t["up"].mul_(router[:, None, :])
+        t["down"].mul_(I ** -1)
+        run()
+        for n in range(T):
+            e = idx[n].long()
+            assert e.tolist() == list(range(n * K, (n + 1) * K))
+            h = (t["up"][e].double() * t["x"][n].double()).sum(-1)
+            want = (weights[n].double()[:, None] * (t["down"][e].double() * h[:, None]).sum(-1)).sum(0)
+            # sums of H, 2 I and K positive products, a step each; h held to 2^-16; one rounding to bf16
+            tol = want * ((2 * I + 2 * K + H + 8) * 2.0 ** -23 + 2.0 ** -16 + 2.0 ** -8)
+            assert bool(((t["out"][n].double() - want).abs() <= tol).all()), n
+
+
+def test_few_token_layer_of_many_experts_and_hidden_elements():
+    # 1024 experts of 2^20 hidden elements: 8192 * 1024 workgroups of 512 threads for the down product
+    import torch
+    T, E, K, H, I = 16, 1024, 64, 1 << 20, 1  # noqa: E741
+    assert E * (H // 128) * 512 >= 1 << 32
+    say("moe layer: 1024 experts of 2^20 hidden elements")
+    with Job(1) as job:
+        t, router, idx, weights, run = _moe(job, T, E, K, H, I)
+        # token n is the unit vector of element n, which alone counts in its logits and its inner value
+        for n in range(T):
+            t["x"][n, n] = 1.0
+            router[n * K:(n + 1) * K, n] = 1.0
+        gen = torch.Generator(device="cuda").manual_seed(4)
+        t["up"][:, 0, :T] = 1.0 + torch.rand((E, T), generator=gen, device="cuda").bfloat16()
+        for e in range(E):
+            t["down"][e, :, 0].normal_(generator=gen)
+        run()
+        for n in range(T):
+            e = idx[n].long()
+            assert sorted(e.tolist()) == list(range(n * K, (n + 1) * K))
+            terms = weights[n].double()[:, None] * t["down"][e, :, 0].double() * t["up"][e, 0, n].double()[:, None]
+            want = terms.sum(0)
+            # K products and sums, a step each, and one rounding to bf16
+            tol = terms.abs().sum(0) * (K + 8) * 2.0 ** -23 + want.abs() * 2.0 ** -8
+            assert bool(((t["out"][n].double() - want).abs() <= tol).all()), n
