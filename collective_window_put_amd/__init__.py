@@ -264,10 +264,12 @@ def _ptr(x) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        if not torch.cuda.is_initialized():
+        # the same stream without a Stream object, which takes 3 us to make: most of a small call's time on the host.
+        # Not part of torch's public interface, so a torch without it takes the public way.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None or not torch.cuda.is_initialized():
             return int(torch.cuda.current_stream().cuda_stream)
-        # the same stream without a Stream object, which takes 3 us to make: most of a small call's time on the host
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
