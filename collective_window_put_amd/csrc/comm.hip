@@ -1282,9 +1282,8 @@ static bool linear_ok(int R, const vrLinearShape* s) {
          s->rows <= (1 << 24) && s->groups >= 1 && s->groups <= 1024 && s->in >= 1 && s->in <= (1 << 20) &&
          s->out >= 1 && s->out <= (1 << 20);
 }
-size_t vr_linear_workspace_bytes(int nranks, const vrLinearShape* s) {
-  return linear_ok(nranks, s) ? linear_workspace_bytes(nranks, *s) : 0;
-}
+// The products keep everything in registers and the LDS.
+size_t vr_linear_workspace_bytes(int, const vrLinearShape*) { return 0; }
 size_t vr_linear_backward_workspace_bytes(int nranks, const vrLinearShape* s) {
   return linear_ok(nranks, s) ? linear_backward_workspace_bytes(nranks, *s) : 0;
 }
@@ -1305,8 +1304,7 @@ struct LinearBytes {
 };
 
 vrResult_t vr_linear(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w, vrSlice bias, vrSlice residual,
-                     const int32_t* group_rows, vrSlice out, vrSlice preact, void* ws, size_t ws_bytes,
-                     void* stream) {
+                     const int32_t* group_rows, vrSlice out, vrSlice preact, void*, size_t, void* stream) {
   if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
   if (!on_device(c)) return VR_ERR_INVALID_USAGE;
   if (!linear_ok(c->nranks, s) || (!group_rows && s->groups > 1)) return VR_ERR_INVALID_ARGUMENT;
@@ -1319,13 +1317,8 @@ vrResult_t vr_linear(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w, v
   if (group_rows && (!dev_span_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out) ||
                      !clear_of(c, group_rows, b.counts, preact, b.z)))
     return VR_ERR_INVALID_ARGUMENT;
-  const size_t need = linear_workspace_bytes(c->nranks, *s);
-  if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
-  if (need)
-    for (const SliceUse& u : use)
-      if (!clear_of(c, ws, need, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
   if (!s->rows) return VR_OK;
-  return launch_linear(c, *s, x, w, bias, residual, group_rows, out, preact, static_cast<char*>(ws), S(stream));
+  return launch_linear(c, *s, x, w, bias, residual, group_rows, out, preact, S(stream));
 }
 
 vrResult_t vr_linear_backward(vrComm_t c, const vrLinearShape* s, vrSlice dout, vrSlice x, vrSlice w, vrSlice preact,

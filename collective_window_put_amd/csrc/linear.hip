@@ -26,7 +26,6 @@ struct GemmArgs {
   uint64_t b_group, out_group;
   int mt, nt;             // row tiles per rank (kDw: per group), column tiles
   int tile0;              // the launch's first tile
-  uint32_t act;
 };
 
 // A tile of ROWS rows and 128 bytes of the contraction axis, or of 128 bytes'
@@ -903,7 +902,6 @@ vrResult_t linear(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrS
   a.O = s.out;
   a.lda = a.ldb = s.in;
   a.b_group = (uint64_t)a.N * s.in;
-  a.act = s.act;
   vrResult_t e = VR_OK;
   with_act(s.act, [&](auto act) {
     e = gated(s) ? launch_gemm<DT, kFwd, act(), true>(a, st) : launch_gemm<DT, kFwd, act(), false>(a, st);
@@ -978,12 +976,11 @@ vrResult_t linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dou
 
 }  // namespace
 
-size_t linear_workspace_bytes(int, const vrLinearShape&) { return 0; }
 size_t linear_backward_workspace_bytes(int R, const vrLinearShape& s) { return backward_layout(R, s).total; }
 
 vrResult_t launch_linear(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrSlice& w, const vrSlice& bias,
                          const vrSlice& residual, const int32_t* group_rows, const vrSlice& out,
-                         const vrSlice& preact, char*, hipStream_t st) {
+                         const vrSlice& preact, hipStream_t st) {
   return s.dtype == VR_DT_F32 ? linear<VR_DT_F32>(c, s, x, w, bias, residual, group_rows, out, preact, st)
                               : linear<VR_DT_BF16>(c, s, x, w, bias, residual, group_rows, out, preact, st);
 }

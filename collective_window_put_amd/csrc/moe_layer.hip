@@ -172,7 +172,6 @@ __global__ __launch_bounds__(1024) void k_moe_route(const MoeArgs a) {
 // token names an expert once at most); returns their count, 0 when there is no
 // such expert. All threads of the workgroup call it.
 __device__ inline int find_expert(const MoeArgs& a, int slot, short* ids, uint32_t* bits, short* list, int* expert) {
-
   const int tid = threadIdx.x, lane = tid & 63, pairs = a.N * a.K;
   if (a.N == 1) {  // one token's experts all differ: the slot is the entry
     *expert = a.topk[slot];

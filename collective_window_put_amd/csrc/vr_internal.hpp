@@ -133,11 +133,10 @@ vrResult_t launch_route(vrComm* c, const vrSlice& logits, int dtype, int T, int 
 vrResult_t launch_route_backward(vrComm* c, const vrSlice& logits, int dtype, int T, int K, int E,
                                  const int32_t* topk, const float* weights, const float* dweights,
                                  const vrSlice& dlogits, bool renorm, hipStream_t st);
-size_t linear_workspace_bytes(int R, const vrLinearShape& s);
 size_t linear_backward_workspace_bytes(int R, const vrLinearShape& s);
 vrResult_t launch_linear(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrSlice& w, const vrSlice& bias,
                          const vrSlice& residual, const int32_t* group_rows, const vrSlice& out,
-                         const vrSlice& preact, char* ws, hipStream_t st);
+                         const vrSlice& preact, hipStream_t st);
 vrResult_t launch_linear_backward(vrComm* c, const vrLinearShape& s, const vrSlice& dout, const vrSlice& x,
                                   const vrSlice& w, const vrSlice& preact, const int32_t* group_rows,
                                   const vrSlice& dx, const vrSlice& dw, const vrSlice& dbias, char* ws,

@@ -649,7 +649,8 @@ typedef struct {
   uint32_t act;
 } vrLinearShape;
 
-/* Device bytes of workspace a call needs; 0 also on invalid arguments. */
+/* Device bytes of workspace a call needs; 0 also on invalid arguments.
+ * vr_linear needs none. */
 size_t vr_linear_workspace_bytes(int nranks, const vrLinearShape* shape);
 size_t vr_linear_backward_workspace_bytes(int nranks, const vrLinearShape* shape);
 
