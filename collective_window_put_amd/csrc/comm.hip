@@ -1338,6 +1338,9 @@ vrResult_t vr_linear_backward(vrComm_t c, const vrLinearShape* s, vrSlice dout, 
   if (group_rows && !dev_span_ok(c, group_rows, b.counts)) return VR_ERR_INVALID_ARGUMENT;
   const size_t need = linear_backward_workspace_bytes(c->nranks, *s);
   if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
+  if (group_rows &&
+      overlap(reinterpret_cast<const char*>(group_rows), b.counts, static_cast<const char*>(ws), need))
+    return VR_ERR_INVALID_ARGUMENT;
   for (const SliceUse& u : use)
     if (!clear_of(c, ws, need, *u.s, u.n) || (u.written && !clear_of(c, group_rows, b.counts, *u.s, u.n)))
       return VR_ERR_INVALID_ARGUMENT;

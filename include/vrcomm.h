@@ -588,9 +588,10 @@ vrResult_t vr_signal_pingpong(vrComm_t comm, vrWindow_t win, size_t off, size_t 
  * boundaries run fastest. VR_DT_F32 and VR_DT_BF16; every sum is held in
  * binary32 or wider, and bf16 outputs are rounded to nearest even once.
  * Workspaces are the caller's: device memory of at least the stated bytes,
- * 256-byte aligned, used until the call's work on the stream has run; calls
- * that may overlap need workspaces of their own. Nothing is allocated, and
- * every call may be captured into a graph as it is. */
+ * 256-byte aligned and clear of the call's other arguments, used until the
+ * call's work on the stream has run; calls that may overlap need workspaces of
+ * their own. Nothing is allocated, and every call may be captured into a graph
+ * as it is. */
 
 /* A tensor's place in a window: rank r's part starts `offset` bytes into its
  * slice. window NULL: the optional tensor is absent (offset is ignored). */
