@@ -7,11 +7,11 @@
 //   renormalized  dx[e_k] = w[k] (dw[k] - m), 0 elsewhere
 //
 // Two forms. K up to 16 and E up to 512: 16 lanes to a token, four tokens to a
-// wave (k_route_rows, below). Else one wave takes a token: lane l holds the V = ceil(E / 64) (rounded to a
-// power of two) logits of columns l * V ..., so among equal logits the lowest
-// lane, and in it the lowest register, is the lowest expert. Each of the K
-// rounds takes the wave's maximum, finds its owner with a ballot and removes
-// it there; lane k keeps round k's expert.
+// wave (k_route_rows, below). Else one wave takes a token: lane l holds the
+// V = ceil(E / 64) (rounded to a power of two) logits of columns l * V ..., so
+// among equal logits the lowest lane, and in it the lowest register, is the
+// lowest expert. Each of the K rounds takes the wave's maximum, finds its owner
+// with a ballot and removes it there; lane k keeps round k's expert.
 #include <hip/hip_runtime.h>
 
 #include "vr_layers.hpp"
@@ -187,8 +187,10 @@ __global__ __launch_bounds__(kThreads) void k_route_backward(const RouteArgs a) 
 // Lane s of a row of 16 holds V columns of its token in pieces of P, the row's
 // lanes side by side. 32768 tokens of 256 fp32 logits, K = 8: 25.7 us with a
 // wave to a token, whose K rounds of maximum, ballot and removal are bound by
-// the vector units; 10.7 us this way (7.2 us at a large copy's rate). The
-// gradient of 32768 x 256 bf16 logits: 20.7 and 11.5 us (7.4).
+// the vector units; 10.2 us this way (5.4 us at a large copy's 6.55 TB/s). The
+// gradient of 32768 x 256 bf16 logits: 20.7 and 11.5 us (5.6); half the active
+// LDS cycles of k_route_backward_rows are bank conflicts, since the four rows of
+// a wave in `adds` lie a multiple of all banks apart.
 template <int DT, int V> struct Cols {
   static constexpr int P = V < Elem<DT>::kChunk ? V : Elem<DT>::kChunk;
   __device__ static int at(int j, int s) { return (j / P * 16 + s) * P + j % P; }
@@ -260,7 +262,9 @@ __device__ inline void wave_lds() {
 // logit from below, so only what reaches it (11 of 256 logits for K = 8, on
 // average) goes to a list in the LDS, and each entry's place is the number of
 // entries above it. An entry is the logit's order-preserving bits over the
-// complement of its column: equal logits fall by column.
+// complement of its column: equal logits fall by column. Ties at the bound are
+// all listed: a row of E equal logits compares E entries with E, and 32768 such
+// tokens of 256 logits take 256 us.
 template <int DT, int V>
 __global__ __launch_bounds__(kThreads) void k_route_rows(const RouteArgs a) {
   __shared__ uint64_t lists[kWaves * 4][16 * V];
