@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_int, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_size_t, c_uint32, c_uint64, c_void_p
 
 __all__ = [
     "VrError", "VrLibraryMissing", "LIB_PATH", "lib", "SYMBOLS",
@@ -32,7 +32,7 @@ __all__ = [
     "VR_MOE_LAYER_MAX_TOKENS",
     # argument structures and action helpers
     "vrCommRequirements", "vrRemoteAction", "vrLocalAction", "vrDevComm", "vrDevWindow",
-    "vrSlice", "vrLinearShape", "vrMoeShape",
+    "vrSlice", "vrLinearShape", "vrMoeShape", "vrNormShape",
     "SignalInc", "SignalAdd", "CounterInc", "VASignalInc", "VASignalAdd",
     # entry points
     "vr_error_string", "vr_version", "vr_comm_workspace_bytes", "vr_comm_create", "vr_comm_destroy",
@@ -47,6 +47,8 @@ __all__ = [
     "vr_ring_exchange", "vr_signal_pingpong",
     "vr_route", "vr_route_backward", "vr_linear_workspace_bytes", "vr_linear", "vr_linear_backward_workspace_bytes",
     "vr_linear_backward", "vr_moe_layer_workspace_bytes", "vr_moe_layer",
+    "vr_q8_row_bytes", "vr_norm", "vr_norm_backward_workspace_bytes", "vr_norm_backward", "vr_quantize", "vr_dequantize",
+    "vr_linear_q8", "vr_combine_backward",
 ]
 
 # The in-tree build; VRCOMM_LIB may name another build of the same library.
@@ -138,6 +140,10 @@ class vrMoeShape(Structure):
                 ("topk", c_int), ("act", c_uint32), ("flags", c_uint32)]
 
 
+class vrNormShape(Structure):
+    _fields_ = [("dtype", c_int), ("rows", c_int), ("cols", c_int), ("eps", c_float)]
+
+
 def SignalInc(sig_id: int, strong: bool = True) -> vrRemoteAction:
     return vrRemoteAction(VR_SIGNAL_INC, sig_id, 0, int(strong), 0, None, 0)
 
@@ -220,6 +226,16 @@ SYMBOLS = {
     "vr_moe_layer_workspace_bytes": (c_size_t, [c_int, POINTER(vrMoeShape)]),
     "vr_moe_layer": (_R, [_P, POINTER(vrMoeShape), vrSlice, _P, vrSlice, vrSlice, vrSlice, vrSlice, _P, _P, _P,
                           c_size_t, _P]),
+    "vr_q8_row_bytes": (c_size_t, [c_int]),
+    "vr_norm": (_R, [_P, POINTER(vrNormShape), vrSlice, vrSlice, vrSlice, vrSlice, vrSlice, vrSlice, _P]),
+    "vr_norm_backward_workspace_bytes": (c_size_t, [c_int, POINTER(vrNormShape)]),
+    "vr_norm_backward": (_R, [_P, POINTER(vrNormShape), vrSlice, vrSlice, vrSlice, vrSlice, vrSlice, vrSlice, _P,
+                              c_size_t, _P]),
+    "vr_quantize": (_R, [_P, vrSlice, c_int, c_int, c_int, c_int, _P, vrSlice, _P]),
+    "vr_dequantize": (_R, [_P, vrSlice, c_int, c_int, c_int, c_int, _P, vrSlice, _P]),
+    "vr_linear_q8": (_R, [_P, POINTER(vrLinearShape), vrSlice, vrSlice, vrSlice, vrSlice, _P, vrSlice, _P]),
+    "vr_combine_backward": (_R, [_P, vrSlice, vrSlice, c_size_t, c_size_t, c_int, _P, _P, _P, c_int, c_int, c_int,
+                                 vrSlice, _P, _P]),
 }
 
 _lib = None
@@ -559,3 +575,45 @@ def vr_moe_layer(comm, shape, x, router, w_up, w_down, out, topk_idx, weights, r
     _check(lib().vr_moe_layer(comm, ctypes.byref(shape), _slice(x), _ptr(router), _slice(w_up), _slice(w_down),
                               _slice(residual), _slice(out), _ptr(topk_idx), _ptr(weights), _ptr(workspace),
                               workspace_bytes, _stream(stream)), "vr_moe_layer")
+
+
+def vr_q8_row_bytes(cols) -> int:
+    return lib().vr_q8_row_bytes(cols)
+
+
+def vr_norm(comm, shape, x, gain=None, residual=None, sum=None, out=None, q8=None, stream=None):
+    _check(lib().vr_norm(comm, ctypes.byref(shape), _slice(x), _slice(residual), _slice(gain), _slice(sum), _slice(out),
+                         _slice(q8), _stream(stream)), "vr_norm")
+
+
+def vr_norm_backward_workspace_bytes(nranks, shape) -> int:
+    return lib().vr_norm_backward_workspace_bytes(nranks, ctypes.byref(shape))
+
+
+def vr_norm_backward(comm, shape, dout, h, gain=None, dsum=None, dh=None, dgain=None, workspace=None, workspace_bytes=0,
+                     stream=None):
+    _check(lib().vr_norm_backward(comm, ctypes.byref(shape), _slice(dout), _slice(h), _slice(gain), _slice(dsum),
+                                  _slice(dh), _slice(dgain), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "vr_norm_backward")
+
+
+def vr_quantize(comm, x, dtype, rows, cols, q8, groups=1, group_rows=None, stream=None):
+    _check(lib().vr_quantize(comm, _slice(x), dtype, rows, cols, groups, _ptr(group_rows), _slice(q8), _stream(stream)),
+           "vr_quantize")
+
+
+def vr_dequantize(comm, q8, dtype, rows, cols, x, groups=1, group_rows=None, stream=None):
+    _check(lib().vr_dequantize(comm, _slice(q8), dtype, rows, cols, groups, _ptr(group_rows), _slice(x), _stream(stream)),
+           "vr_dequantize")
+
+
+def vr_linear_q8(comm, shape, x, w, out, bias=None, residual=None, group_rows=None, stream=None):
+    _check(lib().vr_linear_q8(comm, ctypes.byref(shape), _slice(x), _slice(w), _slice(bias), _slice(residual),
+                              _ptr(group_rows), _slice(out), _stream(stream)), "vr_linear_q8")
+
+
+def vr_combine_backward(comm, dout, y, y_capacity_rows, row_bytes, dtype, topk_idx, weights, send_pos, T, K, num_experts,
+                        dy=None, dweights=None, stream=None):
+    _check(lib().vr_combine_backward(comm, _slice(dout), _slice(y), y_capacity_rows, row_bytes, dtype, _ptr(topk_idx),
+                                     _ptr(weights), _ptr(send_pos), T, K, num_experts, _slice(dy), _ptr(dweights),
+                                     _stream(stream)), "vr_combine_backward")

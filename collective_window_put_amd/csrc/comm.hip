@@ -1198,6 +1198,7 @@ struct SliceUse {
   const vrSlice* s;
   size_t n;
   bool written;
+  size_t es = 0;  // alignment, where it is not the call's element size
 };
 // Present slices are in their windows, and what is written overlaps nothing
 // else; `same` (if any) may be the very slice of `same_out`.
@@ -1205,7 +1206,7 @@ static vrResult_t check_slices(vrComm* c, const SliceUse* use, int count, size_t
                                const vrSlice* same_out) {
   for (int i = 0; i < count; ++i) {
     if (!use[i].s->window) continue;
-    const vrResult_t r = check_slice(c, *use[i].s, use[i].n, es);
+    const vrResult_t r = check_slice(c, *use[i].s, use[i].n, use[i].es ? use[i].es : es);
     if (r != VR_OK) return r;
   }
   for (int i = 0; i < count; ++i)
@@ -1396,6 +1397,135 @@ vrResult_t vr_moe_layer(vrComm_t c, const vrMoeShape* s, vrSlice x, const void* 
   }
   return launch_moe_layer(c, *s, x, router, w_up, w_down, residual, out, topk, weights, static_cast<char*>(ws),
                           S(stream));
+}
+
+// ---- what stands around the products -------------------------------------------------------------
+constexpr int kMostRows = 1 << 24, kMostCols = 1 << 20;
+constexpr size_t kQ8Align = 4;  // of a slice of q8 rows: their scales'
+
+size_t vr_q8_row_bytes(int cols) { return cols >= 1 && cols <= kMostCols ? q8_row_bytes(cols) : 0; }
+
+static bool norm_ok(int R, const vrNormShape* s) {
+  return R >= 1 && R <= VR_MAX_RANKS && s && elem_ok(s->dtype) && s->rows >= 0 && s->rows <= kMostRows && s->cols >= 1 &&
+         s->cols <= kMostCols && s->eps >= 0x1p-126f && s->eps <= 0x1.fffffep127f;
+}
+
+vrResult_t vr_norm(vrComm_t c, const vrNormShape* s, vrSlice x, vrSlice residual, vrSlice gain, vrSlice sum,
+                   vrSlice out, vrSlice q8, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!norm_ok(c->nranks, s) || !x.window || (!out.window && !q8.window) || (sum.window && !residual.window))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t es = s->dtype == VR_DT_F32 ? 4 : 2, n = es * s->rows * s->cols;
+  const SliceUse use[] = {{&x, n, false},  {&residual, n, false}, {&gain, es * s->cols, false},
+                          {&sum, n, true}, {&out, n, true},       {&q8, q8_row_bytes(s->cols) * s->rows, true, kQ8Align}};
+  const vrResult_t r = check_slices(c, use, 6, es, &residual, &sum);
+  if (r != VR_OK) return r;
+  if (!s->rows) return VR_OK;
+  return launch_norm(c, *s, x, residual, gain, sum, out, q8, S(stream));
+}
+
+size_t vr_norm_backward_workspace_bytes(int nranks, const vrNormShape* s) {
+  return norm_ok(nranks, s) ? norm_backward_workspace_bytes(nranks, *s) : 0;
+}
+
+vrResult_t vr_norm_backward(vrComm_t c, const vrNormShape* s, vrSlice dout, vrSlice h, vrSlice gain, vrSlice dsum,
+                            vrSlice dh, vrSlice dgain, void* ws, size_t ws_bytes, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!norm_ok(c->nranks, s) || !dout.window || !h.window || (!dh.window && !dgain.window))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t es = s->dtype == VR_DT_F32 ? 4 : 2, n = es * s->rows * s->cols, m = es * s->cols;
+  const SliceUse use[] = {{&dout, n, false}, {&h, n, false}, {&gain, m, false},
+                          {&dsum, n, false}, {&dh, n, true}, {&dgain, m, true}};
+  const vrResult_t r = check_slices(c, use, 6, es, &dsum, &dh);
+  if (r != VR_OK) return r;
+  const size_t need = norm_backward_workspace_bytes(c->nranks, *s);
+  if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
+  for (const SliceUse& u : use)
+    if (!clear_of(c, ws, need, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
+  return launch_norm_backward(c, *s, dout, h, gain, dsum, dh, dgain, static_cast<char*>(ws), S(stream));
+}
+
+// Rows of [rows][cols] elements on one side, q8 rows on the other; `back`: from the q8 rows.
+static vrResult_t rows_in_8_bits(vrComm_t c, const vrSlice& x, int dtype, int rows, int cols, int groups,
+                                 const int32_t* group_rows, const vrSlice& q8, bool back, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  if (!elem_ok(dtype) || rows < 0 || rows > kMostRows || cols < 1 || cols > kMostCols || groups < 1 || groups > 1024 ||
+      (!group_rows && groups > 1) || !x.window || !q8.window)
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype == VR_DT_F32 ? 4 : 2, n = es * rows * cols, n8 = q8_row_bytes(cols) * rows;
+  const size_t counts = sizeof(int32_t) * c->nranks * groups;
+  const SliceUse use[] = {{&x, n, back}, {&q8, n8, !back, kQ8Align}};
+  const vrResult_t r = check_slices(c, use, 2, es, nullptr, nullptr);
+  if (r != VR_OK) return r;
+  if (group_rows && (!dev_span_ok(c, group_rows, counts) || !clear_of(c, group_rows, counts, back ? x : q8, back ? n : n8)))
+    return VR_ERR_INVALID_ARGUMENT;
+  if (!rows) return VR_OK;
+  return back ? launch_dequantize(c, q8, dtype, rows, cols, groups, group_rows, x, S(stream))
+              : launch_quantize(c, x, dtype, rows, cols, groups, group_rows, q8, S(stream));
+}
+vrResult_t vr_quantize(vrComm_t c, vrSlice x, int dtype, int rows, int cols, int groups, const int32_t* group_rows,
+                       vrSlice q8, void* stream) {
+  return rows_in_8_bits(c, x, dtype, rows, cols, groups, group_rows, q8, false, stream);
+}
+vrResult_t vr_dequantize(vrComm_t c, vrSlice q8, int dtype, int rows, int cols, int groups, const int32_t* group_rows,
+                         vrSlice x, void* stream) {
+  return rows_in_8_bits(c, x, dtype, rows, cols, groups, group_rows, q8, true, stream);
+}
+
+vrResult_t vr_linear_q8(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w, vrSlice bias, vrSlice residual,
+                        const int32_t* group_rows, vrSlice out, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  // 131071 products of two bytes, 2^14 at most each, stay below 2^31
+  if (!linear_ok(c->nranks, s) || s->in > 131071 || (!group_rows && s->groups > 1)) return VR_ERR_INVALID_ARGUMENT;
+  if (!x.window || !w.window || !out.window) return VR_ERR_INVALID_ARGUMENT;
+  const LinearBytes b(c->nranks, *s);
+  const size_t row = q8_row_bytes(s->in), n = (size_t)s->out * ((s->act & VR_ACT_GATED) ? 2 : 1);
+  const SliceUse use[] = {{&x, row * s->rows, false, kQ8Align}, {&w, row * s->groups * n, false, kQ8Align},
+                          {&bias, b.bias, false},               {&residual, b.out, false},
+                          {&out, b.out, true}};
+  const vrResult_t r = check_slices(c, use, 5, b.es, &residual, &out);
+  if (r != VR_OK) return r;
+  if (group_rows && (!dev_span_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out)))
+    return VR_ERR_INVALID_ARGUMENT;
+  if (!s->rows) return VR_OK;
+  return launch_linear_q8(c, *s, x, w, bias, residual, group_rows, out, S(stream));
+}
+
+vrResult_t vr_combine_backward(vrComm_t c, vrSlice dout, vrSlice y, size_t cap, size_t row_bytes, int dtype,
+                               const int32_t* topk, const float* weights, const int32_t* send_pos, int T, int K, int E,
+                               vrSlice dy, float* dweights, void* stream) {
+  if (!live(c)) return VR_ERR_INVALID_ARGUMENT;
+  if (!on_device(c)) return VR_ERR_INVALID_USAGE;
+  const int R = c->nranks;
+  if (!elem_ok(dtype) || T < 0 || T >= 65536 || K < 1 || K > 64 || E < R || E % R || E > 1024)
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype == VR_DT_F32 ? 4 : 2, m = (size_t)R * T * K * 4;
+  if (row_bytes == 0 || row_bytes > (size_t(1) << 30) || row_bytes % es || cap > (size_t(1) << 31))
+    return VR_ERR_INVALID_ARGUMENT;
+  if (!dout.window || (!dy.window && !dweights) || (dweights && !y.window)) return VR_ERR_INVALID_ARGUMENT;
+  const SliceUse use[] = {{&dout, row_bytes * T, false}, {&y, row_bytes * cap, false}, {&dy, row_bytes * cap, true}};
+  const vrResult_t r = check_slices(c, use, 3, es, nullptr, nullptr);
+  if (r != VR_OK) return r;
+  if (!T) return VR_OK;
+  const struct {
+    const void* p;
+    bool written;
+  } arr[] = {{topk, false}, {weights, false}, {send_pos, false}, {dweights, true}};
+  for (int i = 0; i < 4; ++i) {
+    if (i == 3 && !dweights) break;
+    if (reinterpret_cast<uintptr_t>(arr[i].p) % 4 || !dev_span_ok(c, arr[i].p, m)) return VR_ERR_INVALID_ARGUMENT;
+    for (const SliceUse& u : use)
+      if ((u.written || arr[i].written) && !clear_of(c, arr[i].p, m, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if (arr[i].written && overlap(static_cast<const char*>(arr[i].p), m, static_cast<const char*>(arr[j].p), m))
+        return VR_ERR_INVALID_ARGUMENT;
+  }
+  return launch_combine_backward(c, dout, y, cap, row_bytes, dtype, topk, weights, send_pos, T, K, E, dy, dweights,
+                                 S(stream));
 }
 
 }  // extern "C"

@@ -146,6 +146,24 @@ vrResult_t launch_moe_layer(vrComm* c, const vrMoeShape& s, const vrSlice& x, co
                             const vrSlice& w_down, const vrSlice& residual, const vrSlice& out, int32_t* topk,
                             float* weights, char* ws, hipStream_t st);
 
+// rows in 8 bits: bytes of a row of cols values
+inline size_t q8_row_bytes(int cols) { return (static_cast<size_t>(cols) + 4 + 127) / 128 * 128; }
+vrResult_t launch_norm(vrComm* c, const vrNormShape& s, const vrSlice& x, const vrSlice& residual, const vrSlice& gain,
+                       const vrSlice& sum, const vrSlice& out, const vrSlice& q8, hipStream_t st);
+size_t norm_backward_workspace_bytes(int R, const vrNormShape& s);
+vrResult_t launch_norm_backward(vrComm* c, const vrNormShape& s, const vrSlice& dout, const vrSlice& h,
+                                const vrSlice& gain, const vrSlice& dsum, const vrSlice& dh, const vrSlice& dgain,
+                                char* ws, hipStream_t st);
+vrResult_t launch_quantize(vrComm* c, const vrSlice& x, int dtype, int rows, int cols, int groups,
+                           const int32_t* group_rows, const vrSlice& q8, hipStream_t st);
+vrResult_t launch_dequantize(vrComm* c, const vrSlice& q8, int dtype, int rows, int cols, int groups,
+                             const int32_t* group_rows, const vrSlice& x, hipStream_t st);
+vrResult_t launch_linear_q8(vrComm* c, const vrLinearShape& s, const vrSlice& x, const vrSlice& w, const vrSlice& bias,
+                            const vrSlice& residual, const int32_t* group_rows, const vrSlice& out, hipStream_t st);
+vrResult_t launch_combine_backward(vrComm* c, const vrSlice& dout, const vrSlice& y, size_t cap, size_t row_bytes,
+                                   int dtype, const int32_t* topk, const float* weights, const int32_t* pos, int T,
+                                   int K, int E, const vrSlice& dy, float* dweights, hipStream_t st);
+
 // The ranks' parts of a slice (nulls when it is absent).
 inline WinTab slice_tab(const vrSlice& s) {
   WinTab t;

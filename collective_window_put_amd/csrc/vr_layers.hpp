@@ -1,5 +1,5 @@
-// Shared by the layer kernels (route.hip, linear.hip, moe_layer.hip): element
-// traits, activations, wave reductions and the row ranges of groups.
+// Shared by the layer kernels (route.hip, linear.hip, linear_q8.hip, moe_layer.hip,
+// norm.hip, combine_grad.hip): element traits, activations, wave reductions and the row ranges of groups.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -44,6 +44,21 @@ template <> struct Elem<VR_DT_BF16> {
   __device__ static void store(void* p, uint64_t i, float f) { static_cast<uint16_t*>(p)[i] = bf16_bits(f); }
   __device__ static float round(float f) { return __uint_as_float(static_cast<uint32_t>(bf16_bits(f)) << 16); }
 };
+
+// Operands in 8 bits (rows with a scale each), by the type of what their products make.
+constexpr int kI8ToF32 = 16, kI8ToBf16 = 17;
+template <int DT> constexpr bool kInt8 = DT == kI8ToF32 || DT == kI8ToBf16;
+template <int DT> constexpr int kOutOf = DT == kI8ToF32 ? VR_DT_F32 : DT == kI8ToBf16 ? VR_DT_BF16 : DT;
+struct Elem8 {
+  typedef uint8_t T;
+  static constexpr int kSize = 1;
+  static constexpr int kChunk = 16;
+};
+template <> struct Elem<kI8ToF32> : Elem8 {};
+template <> struct Elem<kI8ToBf16> : Elem8 {};
+typedef int v4i __attribute__((ext_vector_type(4)));
+// Sums of products.
+template <int DT> using Acc = std::conditional_t<kInt8<DT>, v4i, v4f>;
 
 // N consecutive elements (N * size at most 16 bytes); any element alignment:
 // the global loads and stores of this chip take it.
@@ -315,6 +330,13 @@ __device__ inline v4u load_piece(const char* p, int n) {
   v4u v = {0, 0, 0, 0};
   if (n >= Elem<DT>::kChunk) {
     v = load_whole<DT>(p);
+  } else if (kInt8<DT>) {
+    // the piece is inside its row: the values' end is followed by 4 bytes at least, and a row is a multiple of 128
+    if (n > 0) {
+      v = load_whole<DT>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] &= n >= 4 * j + 4 ? ~0u : n > 4 * j ? (1u << (8 * (n - 4 * j))) - 1 : 0u;
+    }
   } else if (n > 0) {
 #pragma unroll
     for (int j = 0; j < Elem<DT>::kChunk - 1; ++j) {
@@ -339,10 +361,12 @@ __device__ inline float piece_f32(v4u v, int j) {
 // acc[i][j] += sum_k a[i][k] b[j][k] over one 16-byte piece per lane: lane l
 // holds elements k = (l / 16) * piece ... of row i = l % 16 of a and j = l % 16
 // of b; of acc it holds i = (l / 16) * 4 + 0..3, j = l % 16. bf16: 32 k per
-// call, fp32: 16.
+// call, fp32: 16, 8 bits: 64.
 template <int DT>
-__device__ inline v4f mfma_piece(v4u a, v4u b, v4f acc) {
-  if constexpr (DT == VR_DT_BF16) {
+__device__ inline Acc<DT> mfma_piece(v4u a, v4u b, Acc<DT> acc) {
+  if constexpr (kInt8<DT>) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), acc, 0, 0, 0);
+  } else if constexpr (DT == VR_DT_BF16) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), acc, 0, 0, 0);
   } else {
 #pragma unroll
@@ -360,7 +384,7 @@ __device__ inline v4f mfma_piece(v4u a, v4u b, v4f acc) {
 // through the LDS, so the loads never wait for a barrier.
 template <int DT, int NW, int NX, int U>
 __device__ inline void stream_products(const char* const* w, const char* const* x, int k, int k1, int K,
-                                       v4f (*acc)[NX]) {
+                                       Acc<DT> (*acc)[NX]) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kStep = 4 * kC;
   const int q = (lane_id() >> 4) * kC;
   v4u wv[U][NW], xv[U][NX];

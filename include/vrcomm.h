@@ -211,7 +211,7 @@ vrResult_t vr_comm_destroy(vrComm_t comm);
 #define VR_ASYNC_CAPACITY      0x2u
 #define VR_ASYNC_BAD_EXPERT    0x4u
 #define VR_ASYNC_LITMUS        0x8u
-#define VR_ASYNC_BAD_VALUE     0x10u /* a NaN or +inf logit: VR_ERR_DEVICE_CHECK */
+#define VR_ASYNC_BAD_VALUE     0x10u /* a NaN or +inf logit, a NaN or infinity in a row for 8 bits: VR_ERR_DEVICE_CHECK */
 vrResult_t vr_comm_get_async_error(vrComm_t comm, vrResult_t* out, uint32_t* bits);
 
 /* Strong-signal litmus for the collectives (GIN page, strong and weak
@@ -716,6 +716,93 @@ size_t vr_moe_layer_workspace_bytes(int nranks, const vrMoeShape* shape);
 vrResult_t vr_moe_layer(vrComm_t comm, const vrMoeShape* shape, vrSlice x, const void* router, vrSlice w_up,
                         vrSlice w_down, vrSlice residual, vrSlice out, int32_t* topk_idx, float* weights,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- what stands around the products: the norm, rows in 8 bits, the combine's gradient ----
+ * Conventions as for the layers above.
+ *
+ * A row in 8 bits ("q8 row") of cols values: cols int8 values, zeros, and in the
+ * last 4 of its vr_q8_row_bytes(cols) bytes the row's binary32 scale; it stands
+ * for value * scale. Rows are packed, each a multiple of 128 bytes: one
+ * vr_dispatch of rows of vr_q8_row_bytes(cols) bytes moves values and scales
+ * together. Slices of q8 rows start at a multiple of 4 bytes (of 16: fastest).
+ * A row becomes one like this: m its largest magnitude, scale = m / 127, value =
+ * x * (127 / m) rounded to nearest even, each off by at most half a scale. A row
+ * with m below 2^-119 (its scale would be subnormal) gets scale 0 and zeros. A
+ * row with a NaN or an infinity gets scale NaN and zeros, so that everything
+ * computed from it is NaN, and sets VR_ASYNC_BAD_VALUE. */
+
+/* (cols + 4) rounded up to a multiple of 128; 0 unless cols is in 1..2^20. */
+size_t vr_q8_row_bytes(int cols);
+
+/* Rows of every rank for vr_norm and vr_norm_backward: rows up to 2^24, cols
+ * 1..2^20, eps at least 2^-126 and finite. */
+typedef struct {
+  int dtype;
+  int rows;
+  int cols;
+  float eps;
+} vrNormShape;
+
+/* Root-mean-square norm, with the residual's addition before it:
+ *   h = x + residual, rounded to dtype (without residual: x)
+ *   y = h / sqrt(mean over the row of h^2 + eps) * gain
+ *   x [rows][cols]; optional: residual [rows][cols], gain [cols] (absent: ones)
+ *   outputs, at least one of out and q8: sum [rows][cols] = h (needs residual;
+ *   may be residual's own slice), out [rows][cols] = y, q8 [rows] = y as q8 rows
+ *   (from y unrounded)
+ * Statistics are binary32 and do not overflow: a row of finite h has a finite
+ * root. No other ranges may overlap an output (VR_ERR_INVALID_ARGUMENT). */
+vrResult_t vr_norm(vrComm_t comm, const vrNormShape* shape, vrSlice x, vrSlice residual, vrSlice gain,
+                   vrSlice sum, vrSlice out, vrSlice q8, void* stream);
+
+/* Gradients of vr_norm. dout [rows][cols] (y's); h [rows][cols] as the forward
+ * call normed it (sum, or x without a residual); optional: gain [cols], dsum
+ * [rows][cols], what reaches h by other ways (the residual stream's gradient).
+ *   dh [rows][cols] = dsum + (g - n * mean(g * n)) / r, with r the row's root,
+ *   n = h / r, g = dout * gain: the gradient of x and of residual alike; may be
+ *   dsum's own slice
+ *   dgain [cols] = sum over the rank's rows of dout * n (zeros without rows)
+ * At least one of the two is wanted. Sums run in a fixed order. */
+size_t vr_norm_backward_workspace_bytes(int nranks, const vrNormShape* shape);
+vrResult_t vr_norm_backward(vrComm_t comm, const vrNormShape* shape, vrSlice dout, vrSlice h, vrSlice gain,
+                            vrSlice dsum, vrSlice dh, vrSlice dgain, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* x [rows][cols] to q8 [rows] as q8 rows, and back (x rounded to dtype). rows up
+ * to 2^24, cols 1..2^20, groups 1..1024; group_rows: device int32 [R][groups] as
+ * vr_linear takes it, here only its sum counts: rows past the last group are
+ * not written. NULL only when groups is 1: all rows. */
+vrResult_t vr_quantize(vrComm_t comm, vrSlice x, int dtype, int rows, int cols, int groups,
+                       const int32_t* group_rows, vrSlice q8, void* stream);
+vrResult_t vr_dequantize(vrComm_t comm, vrSlice q8, int dtype, int rows, int cols, int groups,
+                         const int32_t* group_rows, vrSlice x, void* stream);
+
+/* vr_linear of q8 rows and q8 weights: out = act(x w^T + bias) + residual.
+ *   shape as vr_linear's, in at most 131071; dtype is that of bias, residual and out
+ *   x [rows] q8 rows of `in` values: a scale for each token
+ *   w [groups][N] q8 rows of `in` values: a scale for each channel
+ *   bias, residual, group_rows, out: as vr_linear
+ * Products of values are summed in 32-bit integers, exactly for any bytes. */
+vrResult_t vr_linear_q8(vrComm_t comm, const vrLinearShape* shape, vrSlice x, vrSlice w, vrSlice bias,
+                        vrSlice residual, const int32_t* group_rows, vrSlice out, void* stream);
+
+/* Gradient of vr_combine; with vr_combine of the rows' gradients and weights of
+ * 1, which is the gradient of vr_dispatch, a routed layer's backward pass.
+ *   dout      rank s's [T] rows of row_bytes (slice, dtype): the gradient of out
+ *   y         rank d's y_capacity_rows rows as vr_combine read them; needed for
+ *             dweights only
+ *   topk_idx, weights, send_pos: device [R][T][K], as vr_combine read them
+ * For every entry (s, t, k) with a row p at rank d = expert / (E/R):
+ *   dy[d][p] = weights[s][t][k] * dout[s][t] (rounded once; slice of
+ *   y_capacity_rows rows; rows that no entry names are not written)
+ *   dweights[s][t][k] = sum of dout[s][t] * y[d][p] (device float [R][T][K]); 0
+ *   for an entry without a row
+ * At least one of the two is wanted. Each row belongs to one entry at most, as
+ * vr_dispatch lays them out. Limits and device checks as vr_combine; no signals
+ * are applied. */
+vrResult_t vr_combine_backward(vrComm_t comm, vrSlice dout, vrSlice y, size_t y_capacity_rows, size_t row_bytes,
+                               int dtype, const int32_t* topk_idx, const float* weights, const int32_t* send_pos,
+                               int T, int K, int num_experts, vrSlice dy, float* dweights, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 """Plain definitions, in binary64, of the layers between the collectives: the
 router, the linear layer (dense or by expert) and the few-token
-mixture-of-experts layer, with their gradients.
+mixture-of-experts layer, with their gradients, the root-mean-square norm, rows
+in 8 bits and the combine's gradient.
 
 Formulas (include/vrcomm.h states the same): softmax and its K largest; the
 product x w^T + b with an activation, a gate and a residual; the layer as the
@@ -13,7 +14,8 @@ import math
 
 import numpy as np
 
-__all__ = ["route", "route_backward", "activation", "linear", "linear_backward", "group_ranges", "moe_layer"]
+__all__ = ["route", "route_backward", "activation", "linear", "linear_backward", "group_ranges", "moe_layer",
+           "norm", "norm_backward", "to_8_bits", "combine_backward"]
 
 
 def route(logits, K: int, renorm: bool):
@@ -130,3 +132,43 @@ def moe_layer(x, router, w_up, w_down, act: str, gated: bool, K: int, renorm: bo
             h = activation(z[:I], act)[0] * (z[I:] if gated else 1.0)
             out[n] += weights[n, k] * (w_down[e] @ h)
     return out + (0.0 if residual is None else np.asarray(residual, np.float64)), idx, weights
+
+
+def norm(h, gain, eps: float):
+    """h / sqrt(mean h^2 + eps) * gain, row by row."""
+    h = np.asarray(h, np.float64)
+    return h / np.sqrt((h * h).mean(-1, keepdims=True) + eps) * (1.0 if gain is None else np.asarray(gain, np.float64))
+
+
+def norm_backward(dout, h, gain, eps: float, dsum=None):
+    """(dh, dgain) of rows h; dsum is what reaches h by other ways."""
+    dout, h = np.asarray(dout, np.float64), np.asarray(h, np.float64)
+    root = np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    n, g = h / root, dout * (1.0 if gain is None else np.asarray(gain, np.float64))
+    dh = (g - n * (g * n).mean(-1, keepdims=True)) / root
+    return dh + (0.0 if dsum is None else np.asarray(dsum, np.float64)), (dout * n).sum(0)
+
+
+def to_8_bits(x):
+    """(int8 values, binary32 scales) of rows of binary32 values, bit for bit: scale m / 127 and the multiplier 127 / m
+    rounded to binary32, the product rounded once; zeros below 2^-119, scale NaN where a value is no number."""
+    x = np.asarray(x, np.float32)
+    m = np.abs(x).max(-1, keepdims=True)
+    bad = ~np.isfinite(x).all(-1, keepdims=True)
+    none = bad | (m < np.float32(2.0 ** -119))
+    m1 = np.where(none, np.float32(1), m).astype(np.float32)
+    value = np.rint(np.where(none, 0, x).astype(np.float64) * (np.float32(127) / m1).astype(np.float64))
+    scale = np.where(bad, np.float32(np.nan), np.where(none, np.float32(0), m1 / np.float32(127)))
+    return value.astype(np.int8), scale[..., 0].astype(np.float32)
+
+
+def combine_backward(dout, y, rank, row, weights):
+    """(rows of dy that an entry names, as {(rank, row): gradient}, dweights) of dout [S][T][H], y [R][rows][H]; rank and
+    row [S][T][K] name an entry's row, -1 for none."""
+    dy, dw = {}, np.zeros(np.shape(weights))
+    for at in np.ndindex(*dw.shape):
+        d, p = int(rank[at]), int(row[at])
+        if d >= 0 and p >= 0:
+            dy[d, p] = float(weights[at]) * np.asarray(dout[at[:2]], np.float64)
+            dw[at] = float(np.dot(np.asarray(dout[at[:2]], np.float64), np.asarray(y[d][p], np.float64)))
+    return dy, dw
