@@ -5,8 +5,13 @@
 //   dweights[s][t][k] = dout[s][t] . y[d][p]     (a get from it)
 //
 // Bound by memory: for each entry one row is read and one written; a token's
-// own row is read once for up to kBatch entries. A group of 2^LOG lanes takes a
-// token; all its entries' loads of a column chunk are in flight together.
+// own row is read once for up to kBatch entries. A workgroup's entries are read
+// together and their rows' addresses kept in the LDS, so that a lane holds no
+// more than the rows' pieces and many waves fit; a group of 2^LOG lanes takes a
+// token, its entries' loads of a column chunk in flight together. 8 ranks x 4096
+// tokens of 512 bytes, top-8 of 256 experts: 57 us, 5.1 TB/s of rows in random
+// places (each lane finding its rows by itself: 106 us, 3 waves to a SIMD; 4 or 8
+// entries at a time, workgroups of 64 to 256 threads: within 2 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -28,53 +33,90 @@ struct GradArgs {
   int R, T, K, per, E;        // per: experts of a rank
 };
 
-template <int DT, int LOG>
+// An address read from the LDS, as one of global memory: the compiler makes
+// flat loads and stores of it otherwise, which wait for the LDS too.
+__device__ inline char* global(const char* p) {
+  return (char*)reinterpret_cast<__attribute__((address_space(1))) char*>(reinterpret_cast<uintptr_t>(p));
+}
+// 16 bytes past the caches, which rows in random places only crowd (the case
+// below: 64 us without, 62 with such stores, 57 with such loads too); any
+// element alignment.
+typedef v4u any_v4u __attribute__((aligned(2)));
+__device__ inline v4u load_once(const char* p) { return __builtin_nontemporal_load(reinterpret_cast<const any_v4u*>(p)); }
+template <int DT>
+__device__ inline void store_once(char* p, const float* f) {
+  v4u v;
+  store_n<DT, Elem<DT>::kChunk>(&v, 0, f);
+  __builtin_nontemporal_store(v, reinterpret_cast<any_v4u*>(p));
+}
+
+// Entries of a workgroup's tokens, in dynamic LDS: [kTok][K] each.
+struct Entries {
+  const char** from;  // the row of y; where there is none, the token's own row of dout (a valid address)
+  char** to;          // the row of dy (without DY: of y), or null
+  float* w;
+  __device__ Entries(char* lds, int n) {
+    from = reinterpret_cast<const char**>(lds);
+    to = reinterpret_cast<char**>(lds + n * sizeof(char*));
+    w = reinterpret_cast<float*>(lds + 2 * n * sizeof(char*));
+  }
+  static size_t bytes(int n) { return n * (2 * sizeof(char*) + sizeof(float)); }
+};
+
+template <int DT, int LOG, bool DY, bool DW, bool WHOLE>  // WHOLE: rows of whole pieces
 __global__ __launch_bounds__(256) void k_combine_back(const GradArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kL = 1 << LOG, kTok = 256 / kL;
-  const int s = blockIdx.x % a.R, l = threadIdx.x & (kL - 1);
-  const int t = blockIdx.x / a.R * kTok + threadIdx.x / kL;
-  if (t >= a.T) return;
-  const int H = static_cast<int>(a.row_bytes / Elem<DT>::kSize);
-  const char* d = a.dout.p[s] + (uint64_t)t * a.row_bytes;
-  const uint64_t e0 = ((uint64_t)s * a.T + t) * a.K;
-  const bool whole = H % kC == 0;
-  for (int k0 = 0; k0 < a.K; k0 += kBatch) {
-    const int n = min(kBatch, a.K - k0);
-    uint64_t at[kBatch];  // the entry's row: byte offset in its rank's part, all ones without one
-    int rank[kBatch];
-    float w[kBatch], dot[kBatch];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const uint64_t g = e0 + k0 + min(q, n - 1);
-      const int e = a.topk[g], p = a.pos[g];
-      w[q] = a.weights[g];
-      at[q] = ~0ull;
-      rank[q] = 0;
-      dot[q] = 0.0f;
-      if (q >= n) continue;
-      if (e != -1 && (e < 0 || e >= a.E)) {
-        if (l == 0) atomic_or_u32(a.err, VR_ASYNC_BAD_EXPERT);
-      } else if (e >= 0 && p != -1) {
-        if (p < 0 || (uint64_t)p >= a.cap) {
-          if (l == 0) atomic_or_u32(a.err, VR_ASYNC_CAPACITY);
-        } else {
-          at[q] = (uint64_t)p * a.row_bytes;
-          rank[q] = e / a.per;
-        }
+  extern __shared__ __align__(16) char lds[];
+  const int s = blockIdx.x % a.R, t0 = blockIdx.x / a.R * kTok, tokens = min(kTok, a.T - t0), K = a.K;
+  const Entries en(lds, kTok * K);
+  const char* dout = a.dout.p[s] + (uint64_t)t0 * a.row_bytes;
+  const uint64_t e0 = ((uint64_t)s * a.T + t0) * K;
+  for (int i = threadIdx.x; i < tokens * K; i += 256) {
+    const int e = a.topk[e0 + i], p = a.pos[e0 + i];
+    en.w[i] = a.weights[e0 + i];
+    const char* from = nullptr;
+    char* to = nullptr;
+    if (e != -1 && (e < 0 || e >= a.E)) {
+      atomic_or_u32(a.err, VR_ASYNC_BAD_EXPERT);
+    } else if (e >= 0 && p != -1) {
+      if (p < 0 || (uint64_t)p >= a.cap) {
+        atomic_or_u32(a.err, VR_ASYNC_CAPACITY);
+      } else {
+        const int d = e / a.per;
+        if (DW) from = a.y.p[d] + (uint64_t)p * a.row_bytes;
+        to = (DY ? a.dy.p[d] : a.y.p[d]) + (uint64_t)p * a.row_bytes;
       }
     }
+    if (DW && !from) {
+      a.dweights[e0 + i] = 0.0f;
+      from = dout + (uint64_t)(i / K) * a.row_bytes;
+    }
+    en.from[i] = from;
+    en.to[i] = to;
+  }
+  __syncthreads();
+  const int l = threadIdx.x & (kL - 1), t = threadIdx.x / kL;
+  if (t >= tokens) return;
+  const int H = static_cast<int>(a.row_bytes / Elem<DT>::kSize);
+  const char* d = dout + (uint64_t)t * a.row_bytes;
+  for (int k0 = 0; k0 < K; k0 += kBatch) {
+    const int n = min(kBatch, K - k0), first = t * K + k0;
+    float dot[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) dot[q] = 0.0f;
     for (int col = l * kC; col < H; col += kL * kC) {
-      const uint64_t off = (uint64_t)col * Elem<DT>::kSize;
-      const v4u dv = whole ? load_whole<DT>(d + off) : load_piece<DT>(d + off, H - col);
+      // the last piece of a row that is no multiple of one starts early: its first `again` elements are another lane's too
+      const int at = WHOLE ? col : max(0, min(col, H - kC)), again = col - at;
+      const uint64_t off = (uint64_t)at * Elem<DT>::kSize;
+      const bool tiny = !WHOLE && H < kC;
+      const v4u dv = tiny ? load_piece<DT>(d, H) : load_whole<DT>(d + off);
       v4u yv[kBatch];
-      if (a.dweights) {
+      if (DW) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-          yv[q] = v4u{0, 0, 0, 0};
-          if (at[q] != ~0ull) {
-            const char* p = a.y.p[rank[q]] + at[q] + off;
-            yv[q] = whole ? load_whole<DT>(p) : load_piece<DT>(p, H - col);
-          }
+          if (q >= n) break;
+          const char* from = global(en.from[first + q]) + off;
+          yv[q] = tiny ? load_piece<DT>(from, H) : load_once(from);
         }
       }
       float f[kC];
@@ -82,41 +124,52 @@ __global__ __launch_bounds__(256) void k_combine_back(const GradArgs a) {
       for (int j = 0; j < kC; ++j) f[j] = piece_f32<DT>(dv, j);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        if (at[q] == ~0ull) continue;
-        if (a.dweights) {
+        if (q >= n) break;
+        if (DW) {
 #pragma unroll
-          for (int j = 0; j < kC; ++j) dot[q] = fmaf(f[j], piece_f32<DT>(yv[q], j), dot[q]);
+          for (int j = 0; j < kC; ++j)
+            if (WHOLE || j >= again) dot[q] = fmaf(f[j], piece_f32<DT>(yv[q], j), dot[q]);
         }
-        if (a.dy.p[0]) {
+        if (DY && en.to[first + q]) {
+          char* to = global(en.to[first + q]);
+          const float w = en.w[first + q];
           float g[kC];
 #pragma unroll
-          for (int j = 0; j < kC; ++j) g[j] = w[q] * f[j];
-          char* p = a.dy.p[rank[q]] + at[q];
-          if (H - col >= kC) {
-            store_n<DT, kC>(p, col, g);
+          for (int j = 0; j < kC; ++j) g[j] = w * f[j];
+          if (!tiny) {
+            store_once<DT>(to + off, g);
           } else {
 #pragma unroll
             for (int j = 0; j < kC - 1; ++j)
-              if (j < H - col) Elem<DT>::store(p, col + j, g[j]);
+              if (j < H) Elem<DT>::store(to, j, g[j]);
           }
         }
       }
     }
-    if (a.dweights) {
+    if (DW) {
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         const float v = lane_reduce<LOG>(dot[q], [](float x, float y) { return x + y; });
-        if (l == 0 && q < n) a.dweights[e0 + k0 + q] = v;
+        // an entry without a row has its zero already
+        if (l == q && q < n && en.to[first + q]) a.dweights[e0 + first + q] = v;
       }
     }
   }
 }
 
-template <int DT, int LOG>
+template <int DT, int LOG, bool WHOLE>
 vrResult_t start(const GradArgs& a, hipStream_t st) {
   constexpr int kTok = 256 >> LOG;
-  hipLaunchKernelGGL((k_combine_back<DT, LOG>), dim3(a.R * ((a.T + kTok - 1) / kTok)), dim3(256), 0, st, a);
+  const dim3 grid(a.R * ((a.T + kTok - 1) / kTok));
+  const size_t lds = Entries::bytes(kTok * a.K);  // at most 40 KiB
+  if (!a.dweights) hipLaunchKernelGGL((k_combine_back<DT, LOG, true, false, WHOLE>), grid, dim3(256), lds, st, a);
+  else if (!a.dy.p[0]) hipLaunchKernelGGL((k_combine_back<DT, LOG, false, true, WHOLE>), grid, dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((k_combine_back<DT, LOG, true, true, WHOLE>), grid, dim3(256), lds, st, a);
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+}
+template <int DT, int LOG>
+vrResult_t start(const GradArgs& a, hipStream_t st) {
+  return a.row_bytes % 16 ? start<DT, LOG, false>(a, st) : start<DT, LOG, true>(a, st);
 }
 template <int DT>
 vrResult_t start_any(const GradArgs& a, hipStream_t st) {
