@@ -5,10 +5,10 @@
 //   dweights[s][t][k] = dout[s][t] . y[d][p]     (a get from it)
 //
 // Bound by memory: for each entry one row is read and one written; a token's
-// own row is read once for up to kBatch entries. A workgroup's entries are read
+// own row is read once for 8 (wide rows: 2) entries. A workgroup's entries are read
 // together and their rows' addresses kept in the LDS, so that a lane holds no
 // more than the rows' pieces and many waves fit; a group of 2^LOG lanes takes a
-// token, its entries' loads of a column chunk in flight together. 8 ranks x 4096
+// token, its entries' loads in flight together. 8 ranks x 4096
 // tokens of 512 bytes, top-8 of 256 experts: 57 us, 5.1 TB/s of rows in random
 // places (each lane finding its rows by itself: 106 us, 3 waves to a SIMD; 4 or 8
 // entries at a time, workgroups of 64 to 256 threads: within 2 us).
@@ -21,7 +21,6 @@
 namespace vr {
 namespace {
 
-constexpr int kBatch = 8;  // entries of a token at a time
 
 struct GradArgs {
   WinTab dout, y, dy;
@@ -63,7 +62,8 @@ struct Entries {
   static size_t bytes(int n) { return n * (2 * sizeof(char*) + sizeof(float)); }
 };
 
-template <int DT, int LOG, bool DY, bool DW, bool WHOLE>  // WHOLE: rows of whole pieces
+// WHOLE: rows of whole pieces. kBatch entries at a time, kCh pieces of each to a lane.
+template <int DT, int LOG, bool DY, bool DW, bool WHOLE, int kBatch, int kCh>
 __global__ __launch_bounds__(256) void k_combine_back(const GradArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kL = 1 << LOG, kTok = 256 / kL;
   extern __shared__ __align__(16) char lds[];
@@ -104,44 +104,55 @@ __global__ __launch_bounds__(256) void k_combine_back(const GradArgs a) {
     float dot[kBatch];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) dot[q] = 0.0f;
-    for (int col = l * kC; col < H; col += kL * kC) {
-      // the last piece of a row that is no multiple of one starts early: its first `again` elements are another lane's too
-      const int at = WHOLE ? col : max(0, min(col, H - kC)), again = col - at;
-      const uint64_t off = (uint64_t)at * Elem<DT>::kSize;
+    for (int col0 = l * kC; col0 < H; col0 += kCh * kL * kC) {
+      uint64_t off[kCh];
+      int again[kCh];
+      v4u dv[kCh], yv[kCh][kBatch];
       const bool tiny = !WHOLE && H < kC;
-      const v4u dv = tiny ? load_piece<DT>(d, H) : load_whole<DT>(d + off);
-      v4u yv[kBatch];
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        // the last piece of a row that is no multiple of one starts early: its first `again` elements are another lane's too
+        const int col = col0 + c * kL * kC, at = max(0, min(col, H - kC));
+        again[c] = col - at;
+        off[c] = (uint64_t)at * Elem<DT>::kSize;
+        dv[c] = tiny ? load_piece<DT>(d, H) : load_whole<DT>(d + off[c]);
+      }
       if (DW) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
           if (q >= n) break;
-          const char* from = global(en.from[first + q]) + off;
-          yv[q] = tiny ? load_piece<DT>(from, H) : load_once(from);
+          const char* from = global(en.from[first + q]);
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) yv[c][q] = tiny ? load_piece<DT>(from, H) : load_once(from + off[c]);
         }
       }
-      float f[kC];
 #pragma unroll
-      for (int j = 0; j < kC; ++j) f[j] = piece_f32<DT>(dv, j);
+      for (int c = 0; c < kCh; ++c) {
+        if (kCh > 1 && again[c] >= kC) break;  // past the end, with all further ones
+        float f[kC];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        if (q >= n) break;
-        if (DW) {
+        for (int j = 0; j < kC; ++j) f[j] = piece_f32<DT>(dv[c], j);
 #pragma unroll
-          for (int j = 0; j < kC; ++j)
-            if (WHOLE || j >= again) dot[q] = fmaf(f[j], piece_f32<DT>(yv[q], j), dot[q]);
-        }
-        if (DY && en.to[first + q]) {
-          char* to = global(en.to[first + q]);
-          const float w = en.w[first + q];
-          float g[kC];
+        for (int q = 0; q < kBatch; ++q) {
+          if (q >= n) break;
+          if (DW) {
 #pragma unroll
-          for (int j = 0; j < kC; ++j) g[j] = w * f[j];
-          if (!tiny) {
-            store_once<DT>(to + off, g);
-          } else {
+            for (int j = 0; j < kC; ++j)
+              if (WHOLE || j >= again[c]) dot[q] = fmaf(f[j], piece_f32<DT>(yv[c][q], j), dot[q]);
+          }
+          if (DY && en.to[first + q]) {
+            char* to = global(en.to[first + q]);
+            const float w = en.w[first + q];
+            float g[kC];
 #pragma unroll
-            for (int j = 0; j < kC - 1; ++j)
-              if (j < H) Elem<DT>::store(to, j, g[j]);
+            for (int j = 0; j < kC; ++j) g[j] = w * f[j];
+            if (!tiny) {
+              store_once<DT>(to + off[c], g);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kC - 1; ++j)
+                if (j < H) Elem<DT>::store(to, j, g[j]);
+            }
           }
         }
       }
@@ -157,19 +168,25 @@ __global__ __launch_bounds__(256) void k_combine_back(const GradArgs a) {
   }
 }
 
-template <int DT, int LOG, bool WHOLE>
+template <int DT, int LOG, bool WHOLE, int kB, int kCh>
 vrResult_t start(const GradArgs& a, hipStream_t st) {
   constexpr int kTok = 256 >> LOG;
   const dim3 grid(a.R * ((a.T + kTok - 1) / kTok));
   const size_t lds = Entries::bytes(kTok * a.K);  // at most 40 KiB
-  if (!a.dweights) hipLaunchKernelGGL((k_combine_back<DT, LOG, true, false, WHOLE>), grid, dim3(256), lds, st, a);
-  else if (!a.dy.p[0]) hipLaunchKernelGGL((k_combine_back<DT, LOG, false, true, WHOLE>), grid, dim3(256), lds, st, a);
-  else hipLaunchKernelGGL((k_combine_back<DT, LOG, true, true, WHOLE>), grid, dim3(256), lds, st, a);
+  if (!a.dweights) hipLaunchKernelGGL((k_combine_back<DT, LOG, true, false, WHOLE, kB, kCh>), grid, dim3(256), lds, st, a);
+  else if (!a.dy.p[0]) hipLaunchKernelGGL((k_combine_back<DT, LOG, false, true, WHOLE, kB, kCh>), grid, dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((k_combine_back<DT, LOG, true, true, WHOLE, kB, kCh>), grid, dim3(256), lds, st, a);
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
 template <int DT, int LOG>
 vrResult_t start(const GradArgs& a, hipStream_t st) {
-  return a.row_bytes % 16 ? start<DT, LOG, false>(a, st) : start<DT, LOG, true>(a, st);
+  // Rows of several pieces to a lane: two entries at a time, four pieces of each, so that loads and stores run along the
+  // rows. 4 x 2048 tokens of 4 KiB, top-4: 60 us, eight entries and one piece 67, four and two 64.
+  if constexpr (LOG == 6) {
+    if (a.row_bytes > 16u << LOG)
+      return a.row_bytes % 16 ? start<DT, LOG, false, 2, 4>(a, st) : start<DT, LOG, true, 2, 4>(a, st);
+  }
+  return a.row_bytes % 16 ? start<DT, LOG, false, 8, 1>(a, st) : start<DT, LOG, true, 8, 1>(a, st);
 }
 template <int DT>
 vrResult_t start_any(const GradArgs& a, hipStream_t st) {
