@@ -19,6 +19,7 @@
 namespace vr {
 namespace {
 
+typedef v4u v4u_any __attribute__((aligned(2)));  // at any element's alignment
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr uint32_t kLeastBits = 0x04000000u;  // 2^-119: 1/127 of less would be subnormal
 
@@ -120,32 +121,85 @@ __device__ inline void store_scale(char* row, int cols, uint64_t row8, int t, co
   }
 }
 
-// Columns of a thread's piece p: pieces of 16 bytes, TPR threads side by side.
+// A thread's piece p of a row of TPR threads side by side, 16 bytes to each. A
+// row that is no multiple of a piece ends in one that starts early: its first
+// `again` elements are another thread's too. All of a piece's (kChunk or more):
+// it is past the end.
+struct Piece {
+  int at, again;
+};
 template <int DT, int TPR>
-__device__ inline int piece_col(int p, int t) { return (p * TPR + t) * Elem<DT>::kChunk; }
-
-// A thread's pieces of a row of cols elements; zeros past its end. Rows of
-// whole pieces are read without a branch (past the end: the last piece, which
-// is blanked).
+__device__ inline Piece piece(int p, int t, int cols) {
+  constexpr int kC = Elem<DT>::kChunk;
+  const int col = (p * TPR + t) * kC, at = min(col, cols - kC);
+  return {at, col - at};
+}
+// A thread's P pieces of a row of at least one piece.
 template <int DT, int TPR, int P>
 __device__ inline void load_row(const char* row, int cols, int t, v4u* v) {
-  constexpr int kC = Elem<DT>::kChunk;
-  if (cols % kC == 0) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) v[p] = load_whole<DT>(row + (size_t)min(piece_col<DT, TPR>(p, t), cols - kC) * Elem<DT>::kSize);
+  for (int p = 0; p < P; ++p) v[p] = load_whole<DT>(row + (size_t)piece<DT, TPR>(p, t, cols).at * Elem<DT>::kSize);
+}
+// How a kernel takes its rows: of any length; of whole pieces; of whole pieces
+// and past the caches, where all that a call reads and writes is more than the
+// last of them holds (256 MiB). There that took 109 to 99 us off the gradients of
+// 8 x 2048 rows of 4096 bf16 and 90 to 79 off 8 x 4096 rows of 2048 to 8 bits; rows
+// that a cache holds it slows (4 x 8192 rows of 512 to 8 bits: 13 to 16 us).
+enum Mode { kAny, kWhole, kStream };
+constexpr int64_t kCacheBytes = 256ll << 20;
+template <int DT, int TPR, int P, int MODE>
+__device__ inline void load_once(const char* row, int cols, int t, v4u* v) {
+  if constexpr (MODE == kStream) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      v[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any*>(row + (size_t)piece<DT, TPR>(p, t, cols).at * Elem<DT>::kSize));
   } else {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int col = piece_col<DT, TPR>(p, t);
-      v[p] = load_piece<DT>(row + (size_t)col * Elem<DT>::kSize, cols - col);
-    }
+    load_row<DT, TPR, P>(row, cols, t, v);
+  }
+}
+template <int DT, int MODE>
+__device__ inline void store_once(char* row, int col, const float* f) {
+  if constexpr (MODE == kStream) {
+    v4u v;
+    store_n<DT, Elem<DT>::kChunk>(&v, 0, f);
+    __builtin_nontemporal_store(v, reinterpret_cast<v4u_any*>(row + (size_t)col * Elem<DT>::kSize));
+  } else {
+    store_n<DT, Elem<DT>::kChunk>(row, col, f);
   }
 }
 template <int DT>
-__device__ inline void widen(v4u v, bool in, float* f) {
+__device__ inline void widen(v4u v, float* f) {
 #pragma unroll
-  for (int j = 0; j < Elem<DT>::kChunk; ++j) f[j] = in ? piece_f32<DT>(v, j) : 0.0f;
+  for (int j = 0; j < Elem<DT>::kChunk; ++j) f[j] = piece_f32<DT>(v, j);
 }
+// f(value, p, j) for the values of h that are this thread's alone. WHOLE: rows of whole pieces.
+template <int DT, int TPR, int P, bool WHOLE, class F>
+__device__ inline void each(int t, int cols, F f) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int again = piece<DT, TPR>(p, t, cols).again;
+    if (WHOLE) {
+      if (again == 0) {
+#pragma unroll
+        for (int j = 0; j < Elem<DT>::kChunk; ++j) f(p, j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Elem<DT>::kChunk; ++j)
+        if (j >= again) f(p, j);
+    }
+  }
+}
+// f(p, first column) for the pieces that are stored.
+template <int DT, int TPR, int P, class F>
+__device__ inline void each_piece(int t, int cols, F f) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const Piece q = piece<DT, TPR>(p, t, cols);
+    if (q.again < Elem<DT>::kChunk) f(p, q.at);
+  }
+}
+// Of the kernels that take rows of any length: the piece at column col, elements past the end not stored.
 template <int DT>
 __device__ inline void store_piece(char* row, int col, int cols, const float* f) {
   constexpr int kC = Elem<DT>::kChunk;
@@ -168,56 +222,57 @@ __device__ inline float down(uint32_t m, bool* bad) {
   return ldexpf(1.0f, 127 - static_cast<int>(m >> 23));
 }
 
+// Threads of a workgroup whose rows take TPR.
+constexpr int threads_of(int tpr) { return tpr == 64 ? 256 : tpr; }
+
 // A row to TPR threads (one wave: four rows to a workgroup), P pieces to a
 // thread. NORM: the norm; else x itself, to 8 bits.
-template <int DT, int TPR, int P, bool NORM>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rows(const RowArgs a) {
-  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = TPR < 256 ? 256 / TPR : 1, kW = TPR / 64;
+template <int DT, int TPR, int P, bool NORM, int MODE>
+__global__ __launch_bounds__(threads_of(TPR)) void k_rows(const RowArgs a) {
+  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = threads_of(TPR) / TPR, kW = TPR / 64;
   __shared__ float red_sum[2][kW];
   __shared__ uint32_t red_max[2][kW];
-  const int r = blockIdx.y, t = threadIdx.x % TPR;
+  const int r = blockIdx.y, t = threadIdx.x % TPR, cols = a.cols;
   const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  v4u gv[P];
+  if (NORM && a.gain.p[r]) load_row<DT, TPR, P>(a.gain.p[r], cols, t, gv);
+  v4u xn[P], rn[P];
+  const auto fetch = [&](int row) {
+    const uint64_t at = (uint64_t)row * cols * kES;
+    load_once<DT, TPR, P, MODE>(a.x.p[r] + at, cols, t, xn);
+    if (NORM && a.residual.p[r]) load_once<DT, TPR, P, MODE>(a.residual.p[r] + at, cols, t, rn);
+  };
+  int flip = 0, row = blockIdx.x * kRows + slot;
+  if (row < a.rows) fetch(row);  // reads on before it is known whether a group holds it
   const int used = used_rows(a.counts, r, a.G, a.rows, a.err);
-  int flip = 0;
-  for (int row = blockIdx.x * kRows + slot; row < used; row += gridDim.x * kRows, flip ^= 1) {
-    const uint64_t at = (uint64_t)row * a.cols * kES;
-    v4u xv[P], rv[P], gv[P];
-    load_row<DT, TPR, P>(a.x.p[r] + at, a.cols, t, xv);
-    if (NORM && a.residual.p[r]) load_row<DT, TPR, P>(a.residual.p[r] + at, a.cols, t, rv);
-    if (NORM && a.gain.p[r]) load_row<DT, TPR, P>(a.gain.p[r], a.cols, t, gv);
+  for (; row < used; row += gridDim.x * kRows, flip ^= 1) {
+    const uint64_t at = (uint64_t)row * cols * kES;
+    v4u xv[P], rv[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) xv[p] = xn[p], rv[p] = rn[p];
+    if (row + (int)gridDim.x * kRows < used) fetch(row + gridDim.x * kRows);
     float h[P][kC];
 #pragma unroll
-    for (int p = 0; p < P; ++p) widen<DT>(xv[p], piece_col<DT, TPR>(p, t) < a.cols, h[p]);
+    for (int p = 0; p < P; ++p) widen<DT>(xv[p], h[p]);
     if constexpr (NORM) {
       if (a.residual.p[r]) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float f[kC];
-          widen<DT>(rv[p], piece_col<DT, TPR>(p, t) < a.cols, f);
+          widen<DT>(rv[p], f);
 #pragma unroll
           for (int j = 0; j < kC; ++j) h[p][j] = Elem<DT>::round(h[p][j] + f[j]);
         }
       }
-      if (a.sum.p[r]) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int col = piece_col<DT, TPR>(p, t);
-          if (col < a.cols) store_piece<DT>(a.sum.p[r] + at, col, a.cols, h[p]);
-        }
-      }
       float ss = 0.0f;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < kC; ++j) ss = fmaf(h[p][j], h[p][j], ss);
+      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { ss = fmaf(h[p][j], h[p][j], ss); });
       ss = row_reduce<TPR>(ss, red_sum[flip], Add());
-      float inv = inverse_root(ss, a.cols, a.eps);
+      // only here: sum may lie where residual does, and where two threads share columns both have read them now
+      if (a.sum.p[r]) each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_once<DT, MODE>(a.sum.p[r] + at, col, h[p]); });
+      float inv = inverse_root(ss, cols, a.eps);
       if (!(ss < INFINITY)) {  // the same in all of the row's threads
         uint32_t m = 0;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int j = 0; j < kC; ++j) m = max(m, magnitude(h[p][j]));
+        each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(h[p][j])); });
         m = row_reduce<TPR>(m, red_max[flip], Max());
         if (TPR > 64) __syncthreads();  // both words are written again
         bool bad;
@@ -227,51 +282,39 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rows(const RowArgs a)
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int j = 0; j < kC; ++j) {
-              h[p][j] *= f;
-              ss = fmaf(h[p][j], h[p][j], ss);
-            }
+            for (int j = 0; j < kC; ++j) h[p][j] *= f;
+          each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { ss = fmaf(h[p][j], h[p][j], ss); });
           ss = row_reduce<TPR>(ss, red_sum[flip], Add());
-          inv = inverse_root(ss, a.cols, a.eps * f * f);
+          inv = inverse_root(ss, cols, a.eps * f * f);
         }
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         float f[kC];
-        if (a.gain.p[r]) widen<DT>(gv[p], piece_col<DT, TPR>(p, t) < a.cols, f);
+        widen<DT>(gv[p], f);
 #pragma unroll
-        for (int j = 0; j < kC; ++j) h[p][j] = h[p][j] * inv * (a.gain.p[r] ? f[j] : 1.0f);
-      }
-      if (a.out.p[r]) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int col = piece_col<DT, TPR>(p, t);
-          if (col < a.cols) store_piece<DT>(a.out.p[r] + at, col, a.cols, h[p]);
+        for (int j = 0; j < kC; ++j) {
+          h[p][j] *= inv;
+          if (a.gain.p[r]) h[p][j] *= f[j];
         }
       }
+      if (a.out.p[r]) each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_n<DT, kC>(a.out.p[r] + at, col, h[p]); });
     }
     if (!NORM || a.q8.p[r]) {
       uint32_t m = 0;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < kC; ++j)
-          if (piece_col<DT, TPR>(p, t) + j < a.cols) m = max(m, magnitude(h[p][j]));
+      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(h[p][j])); });
       m = row_reduce<TPR>(m, red_max[flip], Max());
       const To8 q = to_8(m);
       if (m >= kInfBits && t == 0) atomic_or_u32(a.err, VR_ASYNC_BAD_VALUE);
       char* to = a.q8.p[r] + (uint64_t)row * a.row8;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int col = piece_col<DT, TPR>(p, t);
-        if (col < a.cols) store_bytes<kC>(to, col, a.cols - col, h[p], q);
-      }
-      store_scale(to, a.cols, a.row8, t, q);
+      each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_bytes<kC>(to, col, kC, h[p], q); });
+      store_scale(to, cols, a.row8, t, q);
     }
   }
 }
 
-// Rows too long for registers: a workgroup reads its row again for each step.
+// Rows too long for registers (and those of less than a piece): a workgroup
+// reads its row again for each step.
 constexpr int kLongThreads = 1024;
 template <int DT, bool NORM>
 __global__ __launch_bounds__(kLongThreads) void k_rows_long(const RowArgs a) {
@@ -285,10 +328,10 @@ __global__ __launch_bounds__(kLongThreads) void k_rows_long(const RowArgs a) {
     // h of the piece from column col; after the first step from sum, where that is written (it may be residual's own slice)
     const auto get = [&](int col, bool first, float* h) {
       const char* from = NORM && !first && a.sum.p[r] ? a.sum.p[r] : a.x.p[r];
-      widen<DT>(load_piece<DT>(from + at + (uint64_t)col * kES, a.cols - col), true, h);
+      widen<DT>(load_piece<DT>(from + at + (uint64_t)col * kES, a.cols - col), h);
       if (!NORM || !a.residual.p[r] || from != a.x.p[r]) return;
       float f[kC];
-      widen<DT>(load_piece<DT>(a.residual.p[r] + at + (uint64_t)col * kES, a.cols - col), true, f);
+      widen<DT>(load_piece<DT>(a.residual.p[r] + at + (uint64_t)col * kES, a.cols - col), f);
 #pragma unroll
       for (int j = 0; j < kC; ++j) h[j] = Elem<DT>::round(h[j] + f[j]);
     };
@@ -336,7 +379,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rows_long(const RowArgs a) {
       get(col, false, y);
       if constexpr (NORM) {
         float f[kC];
-        if (a.gain.p[r]) widen<DT>(load_piece<DT>(a.gain.p[r] + (uint64_t)col * kES, a.cols - col), true, f);
+        if (a.gain.p[r]) widen<DT>(load_piece<DT>(a.gain.p[r] + (uint64_t)col * kES, a.cols - col), f);
 #pragma unroll
         for (int j = 0; j < kC; ++j) y[j] = y[j] * by * inv * (a.gain.p[r] ? f[j] : 1.0f);
       }
@@ -373,20 +416,30 @@ uint32_t row_grid(int64_t blocks) { return static_cast<uint32_t>(std::min<int64_
 
 template <int DT, int TPR, int P, bool NORM>
 void start_rows(const RowArgs& a, int R, hipStream_t st) {
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  hipLaunchKernelGGL((k_rows<DT, TPR, P, NORM>), dim3(row_grid((a.rows + kRows - 1) / kRows), R), dim3(TPR < 256 ? 256 : TPR),
-                     0, st, a);
+  constexpr int kRows = threads_of(TPR) / TPR;
+  // Rows of a piece to a lane are little work for a wave: where there are many, 2048 workgroups take several each, the next
+  // row on its way (4 x 8192 rows of 512 to 8 bits, which also count their groups' rows first: 13 to 11 us). Longer rows
+  // lose by it (8 x 4096 rows of 2048: 79 to 84 us).
+  const uint32_t blocks = row_grid((a.rows + kRows - 1) / kRows);
+  const dim3 grid(TPR == 64 && P == 1 ? std::min(blocks, 2048u / R) : blocks, R);
+  const int64_t n = (int64_t)R * a.rows * a.cols;
+  int64_t bytes = n * Elem<DT>::kSize * (1 + (a.residual.p[0] != nullptr) + (a.sum.p[0] != nullptr) + (a.out.p[0] != nullptr));
+  if (a.q8.p[0]) bytes += n;
+  if (a.cols % Elem<DT>::kChunk) hipLaunchKernelGGL((k_rows<DT, TPR, P, NORM, kAny>), grid, dim3(threads_of(TPR)), 0, st, a);
+  else if (bytes > kCacheBytes) hipLaunchKernelGGL((k_rows<DT, TPR, P, NORM, kStream>), grid, dim3(threads_of(TPR)), 0, st, a);
+  else hipLaunchKernelGGL((k_rows<DT, TPR, P, NORM, kWhole>), grid, dim3(threads_of(TPR)), 0, st, a);
 }
 template <int DT, bool NORM>
 vrResult_t start(const RowArgs& a, int R, hipStream_t st) {
   const int pieces = (a.cols + Elem<DT>::kChunk - 1) / Elem<DT>::kChunk;
-  if (pieces <= 64) start_rows<DT, 64, 1, NORM>(a, R, st);
+  if (a.cols < Elem<DT>::kChunk || pieces > 4096)
+    hipLaunchKernelGGL((k_rows_long<DT, NORM>), dim3(row_grid(a.rows), R), dim3(kLongThreads), 0, st, a);
+  else if (pieces <= 64) start_rows<DT, 64, 1, NORM>(a, R, st);
   else if (pieces <= 128) start_rows<DT, 64, 2, NORM>(a, R, st);
   else if (pieces <= 256) start_rows<DT, 64, 4, NORM>(a, R, st);
   else if (pieces <= 512) start_rows<DT, 256, 2, NORM>(a, R, st);
   else if (pieces <= 1024) start_rows<DT, 256, 4, NORM>(a, R, st);
-  else if (pieces <= 4096) start_rows<DT, 1024, 4, NORM>(a, R, st);
-  else hipLaunchKernelGGL((k_rows_long<DT, NORM>), dim3(row_grid(a.rows), R), dim3(kLongThreads), 0, st, a);
+  else start_rows<DT, 1024, 4, NORM>(a, R, st);
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
 
@@ -428,47 +481,53 @@ struct BackArgs {
 
 // A row to TPR threads as above. Workgroup x takes rows x, x + slots, ... (of
 // one wave: four at a time) and keeps its columns' sums for dgain in registers.
-template <int DT, int TPR, int P>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_back(const BackArgs a) {
-  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = TPR < 256 ? 256 / TPR : 1, kW = TPR / 64;
+template <int DT, int TPR, int P, int MODE>
+__global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const BackArgs a) {
+  constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = threads_of(TPR) / TPR, kW = TPR / 64;
   __shared__ float red[2][2][kW];
   __shared__ uint32_t red_max[kW];
-  const int r = blockIdx.y, t = threadIdx.x % TPR;
+  const int r = blockIdx.y, t = threadIdx.x % TPR, cols = a.cols;
   const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const bool gained = a.gain.p[r] != nullptr, more = a.dsum.p[r] != nullptr;
   float acc[P][kC];
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < kC; ++j) acc[p][j] = 0.0f;
   v4u gv[P];
-  if (a.gain.p[r]) load_row<DT, TPR, P>(a.gain.p[r], a.cols, t, gv);
-  int flip = 0;
-  for (int row = blockIdx.x * kRows + slot; row < a.rows; row += gridDim.x * kRows, flip ^= 1) {
-    const uint64_t at = (uint64_t)row * a.cols * kES;
+  if (gained) load_row<DT, TPR, P>(a.gain.p[r], cols, t, gv);
+  v4u hn[P], dn[P], sn[P];
+  const auto fetch = [&](int row) {
+    const uint64_t at = (uint64_t)row * cols * kES;
+    load_once<DT, TPR, P, MODE>(a.h.p[r] + at, cols, t, hn);
+    load_once<DT, TPR, P, MODE>(a.dout.p[r] + at, cols, t, dn);
+    if (more) load_once<DT, TPR, P, MODE>(a.dsum.p[r] + at, cols, t, sn);
+  };
+  int flip = 0, row = blockIdx.x * kRows + slot;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += gridDim.x * kRows, flip ^= 1) {
+    const uint64_t at = (uint64_t)row * cols * kES;
     v4u hv[P], dv[P], sv[P];
-    load_row<DT, TPR, P>(a.h.p[r] + at, a.cols, t, hv);
-    load_row<DT, TPR, P>(a.dout.p[r] + at, a.cols, t, dv);
-    if (a.dsum.p[r]) load_row<DT, TPR, P>(a.dsum.p[r] + at, a.cols, t, sv);
+#pragma unroll
+    for (int p = 0; p < P; ++p) hv[p] = hn[p], dv[p] = dn[p], sv[p] = sn[p];
+    if (row + (int)gridDim.x * kRows < a.rows) fetch(row + gridDim.x * kRows);
+    if constexpr (MODE == kAny && TPR > 64) {
+      // dh may lie where dsum does: where two threads share columns both have read them before the workgroup meets in sums()
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (more) asm volatile("" : "+v"(sv[p]));
+    }
     float by = 1.0f, ss = 0.0f, sg = 0.0f;
-    const auto in = [&](int p) { return piece_col<DT, TPR>(p, t) < a.cols; };
     const auto sums = [&] {
       ss = sg = 0.0f;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float h[kC], d[kC], g[kC];
-        widen<DT>(hv[p], in(p), h);
-        widen<DT>(dv[p], in(p), d);
-        if (a.gain.p[r]) widen<DT>(gv[p], in(p), g);
-#pragma unroll
-        for (int j = 0; j < kC; ++j) {
-          const float hb = h[j] * by;
-          ss = fmaf(hb, hb, ss);
-          sg = fmaf(a.gain.p[r] ? d[j] * g[j] : d[j], hb, sg);
-        }
-      }
+      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) {
+        const float h = piece_f32<DT>(hv[p], j) * by, d = piece_f32<DT>(dv[p], j);
+        ss = fmaf(h, h, ss);
+        sg = fmaf(gained ? d * piece_f32<DT>(gv[p], j) : d, h, sg);
+      });
+      ss = wave_sum(ss);
+      sg = wave_sum(sg);
       if constexpr (TPR > 64) {
-        ss = wave_sum(ss);
-        sg = wave_sum(sg);
         if ((threadIdx.x & 63) == 0) {
           red[flip][0][threadIdx.x >> 6] = ss;
           red[flip][1][threadIdx.x >> 6] = sg;
@@ -481,21 +540,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_back(const BackA
           ss += red[flip][0][w];
           sg += red[flip][1][w];
         }
-      } else {
-        ss = wave_sum(ss);
-        sg = wave_sum(sg);
       }
     };
     sums();
     if (!(ss < INFINITY)) {
       uint32_t m = 0;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float h[kC];
-        widen<DT>(hv[p], in(p), h);
-#pragma unroll
-        for (int j = 0; j < kC; ++j) m = max(m, magnitude(h[j]));
-      }
+      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(piece_f32<DT>(hv[p], j))); });
       m = row_reduce<TPR>(m, red_max, Max());
       if (TPR > 64) __syncthreads();  // red is written again, and red_max by the next such row
       bool bad;
@@ -505,54 +555,45 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_back(const BackA
         sums();
       }
     }
-    const float inv = inverse_root(ss, a.cols, a.eps * by * by);
-    const float mean = sg * inv / static_cast<float>(a.cols);  // of g n
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int col = piece_col<DT, TPR>(p, t);
-      float h[kC], d[kC], g[kC], s[kC];
-      widen<DT>(hv[p], in(p), h);
-      widen<DT>(dv[p], in(p), d);
-      if (a.gain.p[r]) widen<DT>(gv[p], in(p), g);
-      if (a.dsum.p[r]) widen<DT>(sv[p], in(p), s);
+    const float inv = inverse_root(ss, cols, a.eps * by * by);
+    const float mean = sg * inv / static_cast<float>(cols);  // of g n
+    each_piece<DT, TPR, P>(t, cols, [&](int p, int col) {
+      float v[kC];
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const float n = h[j] * by * inv;
-        acc[p][j] = fmaf(d[j], n, acc[p][j]);
-        const float v = ((a.gain.p[r] ? d[j] * g[j] : d[j]) - n * mean) * inv * by;
-        h[j] = a.dsum.p[r] ? v + s[j] : v;
+        const float n = piece_f32<DT>(hv[p], j) * by * inv, d = piece_f32<DT>(dv[p], j);
+        acc[p][j] = fmaf(d, n, acc[p][j]);
+        v[j] = ((gained ? d * piece_f32<DT>(gv[p], j) : d) - n * mean) * inv * by;
+        if (more) v[j] += piece_f32<DT>(sv[p], j);
       }
-      if (a.dh.p[r] && col < a.cols) store_piece<DT>(a.dh.p[r] + at, col, a.cols, h);
-    }
+      if (a.dh.p[r]) store_once<DT, MODE>(a.dh.p[r] + at, col, v);
+    });
   }
   if (!a.partial) return;
-  float* out = a.partial + ((uint64_t)r * a.slots + blockIdx.x) * a.cols;
+  float* out = a.partial + ((uint64_t)r * a.slots + blockIdx.x) * cols;
   if constexpr (kRows > 1) {
-    __shared__ float part[kRows][P * 64 * kC];
+    __shared__ float part[kRows][P * 64 * kC];  // two threads that share a column hold the same sum
+    each_piece<DT, TPR, P>(t, cols, [&](int p, int col) {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int j = 0; j < kC; ++j) part[slot][piece_col<DT, TPR>(p, t) + j] = acc[p][j];
+      for (int j = 0; j < kC; ++j) part[slot][col + j] = acc[p][j];
+    });
     __syncthreads();
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
+    for (int i = threadIdx.x; i < cols; i += 256) {
       float s = part[0][i];
 #pragma unroll
       for (int w = 1; w < kRows; ++w) s += part[w][i];
       out[i] = s;
     }
   } else {
+    each_piece<DT, TPR, P>(t, cols, [&](int p, int col) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int col = piece_col<DT, TPR>(p, t);
-      if (col < a.cols) store_piece<VR_DT_F32>(reinterpret_cast<char*>(out), col, a.cols, acc[p]);
-      if constexpr (kC == 8) {
-        if (col + 4 < a.cols) store_piece<VR_DT_F32>(reinterpret_cast<char*>(out), col + 4, a.cols, acc[p] + 4);
-      }
-    }
+      for (int j = 0; j < kC; j += 4) store_n<VR_DT_F32, 4>(out, col + j, acc[p] + j);
+    });
   }
 }
 
-// Rows too long for registers: dh, and the roots for the sums of dgain.
+// Rows too long for registers (and those of less than a piece): dh, and the
+// roots for the sums of dgain.
 template <int DT>
 __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, T = kLongThreads;
@@ -562,7 +603,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs 
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const uint64_t at = (uint64_t)row * a.cols * kES;
     const auto get = [&](const char* base, uint64_t from, int col, float* f) {
-      widen<DT>(load_piece<DT>(base + from + (uint64_t)col * kES, a.cols - col), true, f);
+      widen<DT>(load_piece<DT>(base + from + (uint64_t)col * kES, a.cols - col), f);
     };
     // g of the piece: dout * gain
     const auto weighted = [&](int col, float* g) {
@@ -644,20 +685,22 @@ __global__ __launch_bounds__(256) void k_dgain_long(const BackArgs a) {
   a.partial[((uint64_t)r * a.slots + blockIdx.x) * a.cols + col] = s;
 }
 
-// dgain of 64 columns: four waves take a quarter of the slots each, in order.
+// dgain of 32 columns: 32 half waves take every 32nd slot each, and their sums
+// are added in order.
 template <int DT>
-__global__ __launch_bounds__(256) void k_dgain(const BackArgs a) {
-  const int r = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-  const int per = (a.slots + 3) / 4, last = min(a.slots, (wave + 1) * per);
+__global__ __launch_bounds__(1024) void k_dgain(const BackArgs a) {
+  const int r = blockIdx.y, lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   const float* p = a.partial + (uint64_t)r * a.slots * a.cols + min(col, a.cols - 1);
   float s = 0.0f;
 #pragma unroll 8
-  for (int i = wave * per; i < last; ++i) s += p[(uint64_t)i * a.cols];
-  __shared__ float part[4][64];
-  part[wave][lane] = s;
+  for (int i = part; i < a.slots; i += 32) s += p[(uint64_t)i * a.cols];
+  __shared__ float sum[32][32];
+  sum[part][lane] = s;
   __syncthreads();
-  if (wave || col >= a.cols) return;
-  Elem<DT>::store(a.dgain.p[r], col, (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
+  if (part || col >= a.cols) return;
+#pragma unroll
+  for (int w = 1; w < 32; ++w) s += sum[w][lane];
+  Elem<DT>::store(a.dgain.p[r], col, s);
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -670,7 +713,8 @@ struct BackLayout {
 BackLayout back_layout(int R, const vrNormShape& s) {
   BackLayout l = {};
   const int n = (s.cols + (s.dtype == VR_DT_F32 ? 4 : 8) - 1) / (s.dtype == VR_DT_F32 ? 4 : 8);
-  if (n <= 64) l.tpr = 64, l.pieces = 1;
+  if (s.cols < (s.dtype == VR_DT_F32 ? 4 : 8)) l.tpr = 0;
+  else if (n <= 64) l.tpr = 64, l.pieces = 1;
   else if (n <= 128) l.tpr = 64, l.pieces = 2;
   else if (n <= 256) l.tpr = 256, l.pieces = 1;
   else if (n <= 512) l.tpr = 256, l.pieces = 2;
@@ -683,16 +727,23 @@ BackLayout back_layout(int R, const vrNormShape& s) {
   return l;
 }
 
+template <int DT, int TPR, int P>
+void start_back(const BackArgs& a, int R, hipStream_t st) {
+  const dim3 grid(a.slots, R);
+  const int64_t bytes = (int64_t)R * a.rows * a.cols * Elem<DT>::kSize * (2 + (a.dsum.p[0] != nullptr) + (a.dh.p[0] != nullptr));
+  if (a.cols % Elem<DT>::kChunk) hipLaunchKernelGGL((k_norm_back<DT, TPR, P, kAny>), grid, dim3(threads_of(TPR)), 0, st, a);
+  else if (bytes > kCacheBytes) hipLaunchKernelGGL((k_norm_back<DT, TPR, P, kStream>), grid, dim3(threads_of(TPR)), 0, st, a);
+  else hipLaunchKernelGGL((k_norm_back<DT, TPR, P, kWhole>), grid, dim3(threads_of(TPR)), 0, st, a);
+}
 template <int DT>
 vrResult_t norm_backward(const BackArgs& a, const BackLayout& l, int R, hipStream_t st) {
   if (a.rows && l.tpr) {
-    const dim3 grid(l.slots, R);
-    if (l.tpr == 64 && l.pieces == 1) hipLaunchKernelGGL((k_norm_back<DT, 64, 1>), grid, dim3(256), 0, st, a);
-    else if (l.tpr == 64) hipLaunchKernelGGL((k_norm_back<DT, 64, 2>), grid, dim3(256), 0, st, a);
-    else if (l.tpr == 256 && l.pieces == 1) hipLaunchKernelGGL((k_norm_back<DT, 256, 1>), grid, dim3(256), 0, st, a);
-    else if (l.tpr == 256) hipLaunchKernelGGL((k_norm_back<DT, 256, 2>), grid, dim3(256), 0, st, a);
-    else if (l.pieces == 1) hipLaunchKernelGGL((k_norm_back<DT, 1024, 1>), grid, dim3(1024), 0, st, a);
-    else hipLaunchKernelGGL((k_norm_back<DT, 1024, 2>), grid, dim3(1024), 0, st, a);
+    if (l.tpr == 64 && l.pieces == 1) start_back<DT, 64, 1>(a, R, st);
+    else if (l.tpr == 64) start_back<DT, 64, 2>(a, R, st);
+    else if (l.tpr == 256 && l.pieces == 1) start_back<DT, 256, 1>(a, R, st);
+    else if (l.tpr == 256) start_back<DT, 256, 2>(a, R, st);
+    else if (l.pieces == 1) start_back<DT, 1024, 1>(a, R, st);
+    else start_back<DT, 1024, 2>(a, R, st);
   } else if (a.rows) {
     hipLaunchKernelGGL((k_norm_back_long<DT>), dim3(row_grid(a.rows), R), dim3(kLongThreads), 0, st, a);
     if (a.partial) hipLaunchKernelGGL((k_dgain_long<DT>), dim3(l.slots, (a.cols + 255) / 256, R), dim3(256), 0, st, a);
@@ -700,7 +751,7 @@ vrResult_t norm_backward(const BackArgs& a, const BackLayout& l, int R, hipStrea
   if (a.partial) {
     BackArgs d = a;
     if (!a.rows) d.slots = 0;  // no sums were written: zeros
-    hipLaunchKernelGGL((k_dgain<DT>), dim3((a.cols + 63) / 64, R), dim3(256), 0, st, d);
+    hipLaunchKernelGGL((k_dgain<DT>), dim3((a.cols + 31) / 32, R), dim3(1024), 0, st, d);
   }
   return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
 }
