@@ -158,11 +158,14 @@ __device__ inline v4f from_raw4(typename Raw4<DT>::T v) {
 // compiler keeps their order, and a fragment at a time each load's latency was
 // waited for in turn (82 of the 300 us of a dense 8192 x 4096 x 4096
 // product).
-template <int DT, int ACT, bool GATED, int NF, int MF>
+// PAIRS: fragments 2 p and 2 p + 1 hold the columns 32 p + 8 q + 0..3 and + 4..7 of
+// lane quarter q, not 16 each: 16-byte stores of bf16 rather than 8.
+template <int DT, int ACT, bool GATED, int NF, int MF, bool PAIRS>
 __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0, int m0, int mEnd, int c0, int lane,
                                       const v4f (*acc)[MF]) {
   constexpr int kES = Elem<DT>::kSize, NO = GATED ? NF / 2 : NF, S = GATED ? 2 : 1;
-  const int m1 = m0 + (lane & 15), col = c0 + (lane >> 4) * 4;
+  const int m1 = m0 + (lane & 15), col = c0 + (lane >> 4) * (PAIRS ? 8 : 4);
+  const auto off = [](int i) { return PAIRS ? (i >> 1) * 32 + (i & 1) * 4 : i * 16; };
   // rows whose residual is held at once: all of a small tile's, 32 registers
   constexpr int kRows = MF <= 4 ? MF : 4;
   typename Raw4<DT>::T bias[NO][S], res[kRows][NO];
@@ -174,7 +177,7 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
-      for (int h = 0; h < S; ++h) bias[i][h] = load_raw4<DT>(pb + (uint64_t)(h * a.O + i * 16) * kES);
+      for (int h = 0; h < S; ++h) bias[i][h] = load_raw4<DT>(pb + (uint64_t)(h * a.O + off(i)) * kES);
   }
 #pragma unroll
   for (int j0 = 0; j0 < MF; j0 += kRows) {
@@ -183,15 +186,16 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
       for (int v = 0; v < kRows; ++v)
 #pragma unroll
         for (int i = 0; i < NO; ++i)
-          res[v][i] = load_raw4<DT>(pr + ((uint64_t)(row0 + min(m1 + (j0 + v) * 16, mEnd - 1)) * a.O + col + i * 16) * kES);
+          res[v][i] = load_raw4<DT>(pr + ((uint64_t)(row0 + min(m1 + (j0 + v) * 16, mEnd - 1)) * a.O + col + off(i)) * kES);
     }
 #pragma unroll
     for (int v = 0; v < kRows; ++v) {
       const uint64_t row = row0 + m1 + (j0 + v) * 16;
       if (m1 + (j0 + v) * 16 < mEnd) {
+        float pair[8];
 #pragma unroll
         for (int i = 0; i < NO; ++i) {
-          float z[S][4], y[4];
+          float z[S][4], *y = pair + (PAIRS ? (i & 1) * 4 : 0);
 #pragma unroll
           for (int h = 0; h < S; ++h) {
 #pragma unroll
@@ -201,7 +205,7 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 #pragma unroll
               for (int q = 0; q < 4; ++q) z[h][q] += f[q];
             }
-            if (pz) store_n<DT, 4>(pz, row * a.N + h * a.O + col + i * 16, z[h]);
+            if (pz) store_n<DT, 4>(pz, row * a.N + h * a.O + col + off(i), z[h]);
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -213,7 +217,8 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 #pragma unroll
             for (int q = 0; q < 4; ++q) y[q] += f[q];
           }
-          store_n<DT, 4>(a.out.p[r], row * a.O + col + i * 16, y);
+          if (!PAIRS) store_n<DT, 4>(a.out.p[r], row * a.O + col + off(i), y);
+          else if (i & 1) store_n<DT, 8>(a.out.p[r], row * a.O + col + off(i - 1), pair);
         }
       }
     }
@@ -240,6 +245,16 @@ __device__ inline void load_lds16(const char* base, uint32_t off, char* to) {
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform) : "memory");
 }
 
+// 4 bytes per lane from p straight into the LDS at `to` + lane (`to` the same in
+// all lanes); as load_lds16 otherwise, but the address is a vector's: one wait
+// state between m0's write and its use.
+__device__ inline void load_lds4(const char* p, float* to) {
+  const uint32_t lds = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) float*)(to)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+}
+
 // Workgroups of consecutive numbers run on the XCDs in turn; give each XCD
 // consecutive tiles, which share rows of a and b in its L2.
 __device__ inline int xcd_order(int b, int n) {
@@ -262,6 +277,7 @@ struct Gemm {
   static constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kK = TA::kK;
   static constexpr int kPA = TA::kPieces / kThreads, kPB = TB::kPieces / kThreads;
   static constexpr int kMF = WM / 16, kNF = WN / 16;
+  static constexpr bool kPairs = kInt8<DT> && (GATED ? kNF / 2 : kNF) % 2 == 0;
   static constexpr int kStage = TA::kBytes + TB::kBytes, kStages = !DIRECT || kThreads == 512 ? 2 : STAGES;
 
   struct Where {
@@ -275,8 +291,9 @@ struct Gemm {
     int r, g, row0;
   };
   // Tile b: tiles of a group (kDw) or rank, then groups and
-  // ranks. False when there is no such tile.
-  __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s) {
+  // ranks. False when there is no such tile. find(r, slot): the group of a row tile.
+  template <class F>
+  __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s, F find) {
     Where& t = s->t;
     int nti = b % a.nt, slot = b / a.nt % a.mt;
     b /= a.nt * a.mt;
@@ -296,7 +313,7 @@ struct Gemm {
       t.mEnd = a.M;
     } else {
       s->r = b;
-      const GroupTile q = find_group<false>(a.counts ? a.counts + (size_t)s->r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
+      const GroupTile q = find(s->r, slot);
       if (q.g < 0) return false;
       s->g = q.g;
       s->row0 = q.first;
@@ -317,12 +334,18 @@ struct Gemm {
     return true;
   }
 
+  __device__ static __forceinline__ bool locate(const GemmArgs& a, int b, Spot* s) {
+    return locate(a, b, s, [&](int r, int slot) {
+      return find_group<false>(a.counts ? a.counts + (size_t)r * a.G : nullptr, a.G, a.rows, BM, slot, a.err);
+    });
+  }
+
   template <int ACT>
   __device__ static __forceinline__ void finish(const GemmArgs& a, const Spot& s, int wm, int wn, int lane, const v4f (*acc)[kMF]) {
     const Where& t = s.t;
     if constexpr (MODE == kFwd) {
       if (GATED ? t.n0 / 2 + BN / 2 <= a.O : t.n0 + BN <= a.N) {
-        epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, GATED ? (t.n0 + wn) / 2 : t.n0 + wn, lane, acc);
+        epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, GATED ? (t.n0 + wn) / 2 : t.n0 + wn, lane, acc);
         return;
       }
     }
@@ -334,7 +357,8 @@ struct Gemm {
 #pragma unroll
       for (int i = 0; i < kNF; i += GATED ? 2 : 1) {
         if constexpr (MODE == kFwd) {
-          const int col = GATED ? t.n0 / 2 + (wn + i * 16) / 2 + cq : t.n0 + wn + i * 16 + cq;
+          const int io = GATED ? i / 2 : i, c0 = GATED ? (t.n0 + wn) / 2 : t.n0 + wn;
+          const int col = c0 + (kPairs ? (io >> 1) * 32 + cq * 2 + (io & 1) * 4 : io * 16 + cq);
           epilogue<kOutOf<DT>, ACT, GATED>(a, s.r, s.g, s.row0 + m, col, acc[i][j], acc[i + (GATED ? 1 : 0)][j]);
         } else {
           const int col = t.n0 + wn + i * 16 + cq;
@@ -348,24 +372,27 @@ struct Gemm {
     }
   }
 
-  // Products of rows in 8 bits times the scales of their rows, the last 4 bytes of each.
-  __device__ static __forceinline__ void scaled(const Where& t, int wm, int wn, int lane, const Acc<DT> (*acc)[kMF], v4f (*z)[kMF]) {
+  // The scales of a tile's rows of a and b, the last 4 bytes of each, on their
+  // way into the LDS before anything else is, so that the first step's wait
+  // covers them. (Read from memory by the epilogue they took up to 45 us of 233 at
+  // 8 x 30720 rows, 128 -> 512 gated.) kThreads >= BM and >= BN.
+  static constexpr int kScales = kInt8<DT> ? BM + BN : 0;  // floats
+  __device__ static __forceinline__ void fetch_scales(const Where& t, int tid, int wave, float* to) {
+    if (wave < BM / 64)
+      load_lds4(t.pa + (uint64_t)(min(t.m0 + tid, t.mEnd - 1) - t.m0 + 1) * t.lda - 4, to + wave * 64);
+    if (wave < BN / 64) {
+      bool in;
+      const int n = b_row(t, tid, &in);  // where there is no such row, the tile's first: not stored
+      load_lds4(t.pb + (in ? n - (GATED ? t.n0 / 2 : t.n0) + 1 : 1) * (int64_t)t.ldb - 4, to + BM + wave * 64);
+    }
+  }
+  __device__ static __forceinline__ void scaled(const float* scales, int wm, int wn, int lane, const Acc<DT> (*acc)[kMF], v4f (*z)[kMF]) {
     float sx[kMF];
 #pragma unroll
-    for (int j = 0; j < kMF; ++j) {
-      const int m = min(t.m0 + wm + j * 16 + (lane & 15), t.mEnd - 1);
-      sx[j] = *reinterpret_cast<const float*>(t.pa + (uint64_t)(m - t.m0 + 1) * t.lda - 4);
-    }
+    for (int j = 0; j < kMF; ++j) sx[j] = scales[wm + j * 16 + (lane & 15)];
 #pragma unroll
     for (int i = 0; i < kNF; ++i) {
-      float sw[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bool in;
-        int n = b_row(t, wn + i * 16 + (lane >> 4) * 4 + q, &in);
-        if (!in) n = 0;  // not stored
-        sw[q] = *reinterpret_cast<const float*>(t.pb + (int64_t)(in ? n - (GATED ? t.n0 / 2 : t.n0) + 1 : 1) * (int64_t)t.ldb - 4);
-      }
+      const v4f sw = *reinterpret_cast<const v4f*>(scales + BM + wn + i * 16 + (lane >> 4) * 4);
 #pragma unroll
       for (int j = 0; j < kMF; ++j)
 #pragma unroll
@@ -373,15 +400,18 @@ struct Gemm {
     }
   }
 
-  // Row of b behind tile row j (forward): gated, 16 gate columns, then the same 16 of the other half.
+  // Row of b behind tile row j (forward): gated, 16 gate columns, then the same 16
+  // of the other half. kPairs: the columns as epilogue_whole's PAIRS has them.
   __device__ static __forceinline__ int b_row(const Where& t, int j, bool* in) {
+    const int at = ((j >> 2) & 3) * 8 + (j & 3);
     if constexpr (GATED) {
-      const int o = t.n0 / 2 + (j >> 5) * 16 + (j & 15);
+      const int o = t.n0 / 2 + (kPairs ? (j >> 6) * 32 + at + ((j >> 5) & 1) * 4 : (j >> 5) * 16 + (j & 15));
       *in = o < t.O;
       return o + ((j >> 4) & 1) * t.O;
     } else {
-      *in = t.n0 + j < t.N;
-      return t.n0 + j;
+      const int n = t.n0 + (kPairs ? (j & ~31) + at + ((j >> 4) & 1) * 4 : j);
+      *in = n < t.N;
+      return n;
     }
   }
 
@@ -525,20 +555,24 @@ struct Gemm {
   // In the phase of the first group's R0(t) every read of step t-1 is done:
   // both groups then start loading step t+1 over it, and wait for it at the
   // end of the phase of M1(t), before the first group's R0(t+1).
-  template <bool FIRST>
+  // AHEAD: step 1 is on its way already; both groups load the others behind the
+  // reads of their R0, where waiting to issue holds up no matrix instruction
+  // (8192 x 4096 x 4096 in 8 bits with gelu, bias and residual: 172 to 160 us).
+  template <bool FIRST, bool AHEAD>
   __device__ static __forceinline__ void phases(const Where& t, int steps, int tid, int wave, const uint32_t* oa,
                                                 const uint32_t* ob, char* s0, char* s1, int wm, int wn, int lane,
                                                 Acc<DT> (*acc)[kMF]) {
     if (!FIRST) {
-      if (steps > 1) fetch(t, kK, tid, wave, oa, ob, s1);
+      if (!AHEAD && steps > 1) fetch(t, kK, tid, wave, oa, ob, s1);
       barrier();
     }
     for (int i = 0; i < steps; ++i) {
       char* cur = (i & 1) ? s1 : s0;
       char* nxt = (i & 1) ? s0 : s1;
       v4u fa[kMF], fb[kNF];
-      if (FIRST && i + 1 < steps) fetch(t, (i + 1) * kK, tid, wave, oa, ob, nxt);
+      if (!AHEAD && FIRST && i + 1 < steps) fetch(t, (i + 1) * kK, tid, wave, oa, ob, nxt);
       frags(cur, cur + TA::kBytes, 0, wm, wn, lane, fa, fb);
+      if (AHEAD && i > 0 && i + 1 < steps) fetch(t, (i + 1) * kK, tid, wave, oa, ob, nxt);
       lds_done();
       barrier();
       __builtin_amdgcn_s_setprio(1);
@@ -549,7 +583,7 @@ struct Gemm {
       lds_done();
       if (!FIRST) wait_vmem();
       barrier();
-      if (!FIRST && i + 2 < steps) fetch(t, (i + 2) * kK, tid, wave, oa, ob, cur);
+      if (!AHEAD && !FIRST && i + 2 < steps) fetch(t, (i + 2) * kK, tid, wave, oa, ob, cur);
       __builtin_amdgcn_s_setprio(1);
       products(fa, fb, acc);
       __builtin_amdgcn_s_setprio(0);
@@ -583,13 +617,15 @@ template <int DT, int MODE, int ACT, bool GATED, bool DIRECT, int BM, int BN, in
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmArgs a) {
   using G = Gemm<DT, MODE, GATED, DIRECT, BM, BN, WM, WN, STAGES>;
   constexpr int kK = G::kK, kMF = G::kMF, kNF = G::kNF;
-  __shared__ __align__(16) char s0[G::kStages * G::kStage];
+  __shared__ __align__(16) char s0[G::kStages * G::kStage + G::kScales * 4];
   char* s1 = s0 + G::kStage;
+  float* scales = reinterpret_cast<float*>(s0 + G::kStages * G::kStage);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave % (BM / WM)) * WM, wn = (wave / (BM / WM)) * WN;
   typename G::Spot at;
   if (!G::locate(a, a.tile0 + xcd_order(blockIdx.x, gridDim.x), &at)) return;
   const typename G::Where& t = at.t;
+  if constexpr (kInt8<DT>) G::fetch_scales(t, tid, wave, scales);
 
   Acc<DT> acc[kNF][kMF];
 #pragma unroll
@@ -605,8 +641,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
       if constexpr (G::kThreads == 512) {
         G::fetch(t, 0, tid, wave, oa, ob, s0);
         G::meet();
-        if (wave < 4) G::template phases<true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
-        else G::template phases<false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+        if (wave < 4) G::template phases<true, false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+        else G::template phases<false, false>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
       } else {
         G::ring(t, steps, tid, wave, oa, ob, s0, wm, wn, lane, acc);
       }
@@ -614,6 +650,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
       v4u ra[G::kPA], rb[G::kPB];
       G::load(t, tid, 0, ra, rb);
       G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
+      if constexpr (kInt8<DT>) wait_vmem();  // the scales too
       __syncthreads();
       for (int i = 0; i < steps; ++i)
         G::step(t, (i + 1) * kK, tid, (i & 1) ? s1 : s0, (i & 1) ? s0 : s1, wm, wn, lane, acc);
@@ -623,15 +660,156 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
     v4u ra[G::kPA], rb[G::kPB];
     G::load(t, tid, steps * kK, ra, rb);
     G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
+    if constexpr (kInt8<DT>) wait_vmem();  // the scales too, where no whole step was
     __syncthreads();
     G::multiply(s0, s0 + G::TA::kBytes, wm, wn, lane, acc);
   }
   if constexpr (kInt8<DT>) {
     v4f z[kNF][kMF];
-    G::scaled(t, wm, wn, lane, acc, z);
+    G::scaled(scales, wm, wn, lane, acc, z);
     G::template finish<ACT>(a, at, wm, wn, lane, z);
   } else {
     G::template finish<ACT>(a, at, wm, wn, lane, acc);
+  }
+}
+
+// The groups of a rank in the LDS, for a workgroup that takes many of its tiles:
+// past the last row tile (of bm rows) and the first row of each group. What
+// find_group finds by itself for every tile, about 3000 cycles, is a read and a
+// ballot here.
+struct GroupTable {
+  int32_t *end, *first;  // [G], [G + 1]
+  // By one wave. Counts as find_group takes them, all of them looked at.
+  __device__ void build(const int32_t* counts, int G, int rows, int bm, uint32_t* err) const {
+    const int lane = static_cast<int>(lane_id());
+    int row0 = 0, tile0 = 0;
+    bool bad = false;
+    for (int g0 = 0; g0 < G; g0 += 64) {
+      const int g = g0 + lane, c = g < G ? counts[g] : 0, pos = max(c, 0);
+      int64_t s = pos;  // sums of 64 counts pass 32 bits
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const int64_t o = __shfl_up(s, m);
+        if (lane >= m) s += o;
+      }
+      const int64_t last = s + row0;
+      const int lo = static_cast<int>(last - pos < rows ? last - pos : rows);
+      const int hi = static_cast<int>(last < rows ? last : rows);
+      bad |= c < 0 || last > rows;
+      int k = (hi - lo + bm - 1) / bm;
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const int o = __shfl_up(k, m);
+        if (lane >= m) k += o;
+      }
+      if (g < G) {
+        end[g] = tile0 + k;
+        first[g] = lo;
+        if (g == G - 1) first[G] = hi;
+      }
+      row0 = __builtin_amdgcn_readlane(hi, 63);
+      tile0 += __builtin_amdgcn_readlane(k, 63);
+    }
+    if (ballot(bad) && lane == 0) atomic_or_u32(err, VR_ASYNC_CAPACITY);
+  }
+  // The group that holds row tile `want`.
+  __device__ GroupTile find(int G, int want) const {
+    const int lane = static_cast<int>(lane_id());
+    for (int g0 = 0; g0 < G; g0 += 64) {
+      const uint64_t past = ballot(g0 + lane < G && end[min(g0 + lane, G - 1)] > want);
+      if (!past) continue;
+      const int g = g0 + __builtin_ctzll(past);
+      const int lo = __builtin_amdgcn_readfirstlane(first[g]), hi = __builtin_amdgcn_readfirstlane(first[g + 1]);
+      return {g, lo, hi - lo, g ? __builtin_amdgcn_readfirstlane(end[g - 1]) : 0};
+    }
+    return {-1, 0, 0, 0};
+  }
+};
+
+// 256 x 256 tiles of rows in 8 bits, one workgroup to a compute unit that takes
+// tile after tile: while it finishes one, the next one's first two steps and its
+// scales are on their way. They were issued before the stores, and vector memory
+// operations count down in order, so that the next tile waits for them and not
+// for the stores, where the number of these is known (a whole tile).
+template <int DT, int ACT, bool GATED>
+__global__ __launch_bounds__(512) void k_gemm_run(const GemmArgs a, int tiles) {
+  using G = Gemm<DT, kFwd, GATED, true, 256, 256, 128, 64, 2>;
+  constexpr int kK = G::kK, kMF = G::kMF, kNF = G::kNF;
+  // stores of a wave's part of a whole tile, at least (fp32: twice as many)
+  constexpr int kLoads = G::kPA + G::kPB, kStores = kMF * (GATED ? kNF / 2 : kNF) / 2;
+  static_assert(G::kPairs && kLoads + kStores < 64, "what a wait counts");
+  __shared__ __align__(16) char s0[2 * G::kStage + 2 * G::kScales * 4 + (2 * 1024 + 1) * 4];
+  char* s1 = s0 + G::kStage;
+  float* scales = reinterpret_cast<float*>(s0 + 2 * G::kStage);
+  int32_t* words = reinterpret_cast<int32_t*>(scales + 2 * G::kScales);
+  const GroupTable table = {words, words + 1024};
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave % 2) * 128, wn = (wave / 2) * 64;
+  // an XCD's tiles are consecutive, and so are those that run on it at a time
+  const int x = blockIdx.x & 7, q = tiles >> 3, rem = tiles & 7, stride = gridDim.x >> 3;
+  const int end = (x + 1) * q + min(x + 1, rem);
+  int b = x * q + min(x, rem) + (blockIdx.x >> 3), rank = -1;
+  const auto next = [&](typename G::Spot* s) {  // the same in all waves, and none is in the table's use when it is built
+    for (; b < end; b += stride) {
+      if (G::locate(a, b, s, [&](int r, int slot) {
+            if (!a.counts) return find_group<false>(nullptr, a.G, a.rows, 256, slot, a.err);
+            if (r != rank) {
+              rank = r;
+              __syncthreads();
+              if (wave == 0) table.build(a.counts + (size_t)r * a.G, a.G, a.rows, 256, a.err);
+              __syncthreads();
+            }
+            return table.find(a.G, slot);
+          }))
+        return true;
+    }
+    return false;
+  };
+  const int steps = a.K / kK;
+  uint32_t oa[G::kPA], ob[G::kPB];
+  const auto issue = [&](const typename G::Where& t, float* to) {
+    G::fetch_scales(t, tid, wave, to);
+    G::offsets(t, tid, oa, ob);
+    if (steps > 0) G::fetch(t, 0, tid, wave, oa, ob, s0);
+    if (steps > 1) G::fetch(t, kK, tid, wave, oa, ob, s1);
+  };
+  typename G::Spot at;
+  if (!next(&at)) return;
+  issue(at.t, scales);
+  bool whole = false;  // the tile before was
+  for (int flip = 0;; flip ^= 1) {
+    const typename G::Where& t = at.t;
+    Acc<DT> acc[kNF][kMF];
+#pragma unroll
+    for (int i = 0; i < kNF; ++i)
+#pragma unroll
+      for (int j = 0; j < kMF; ++j) acc[i][j] = Acc<DT>{0, 0, 0, 0};
+    if (steps > 0) {
+      if (steps > 1 && whole) G::template meet<kLoads + kStores>();  // step 0 has landed, all that is older too
+      else G::template meet<0>();
+      if (wave < 4) G::template phases<true, true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+      else G::template phases<false, true>(t, steps, tid, wave, oa, ob, s0, s1, wm, wn, lane, acc);
+    }
+    if (steps * kK < t.K) {
+      v4u ra[G::kPA], rb[G::kPB];
+      G::load(t, tid, steps * kK, ra, rb);
+      G::store(tid, s0, s0 + G::TA::kBytes, ra, rb);
+      wait_vmem();  // the scales too, where no whole step was
+      __syncthreads();
+      G::multiply(s0, s0 + G::TA::kBytes, wm, wn, lane, acc);
+      __syncthreads();
+    }
+    b += stride;
+    typename G::Spot then;
+    const bool more = next(&then);
+    // every wave is past its reads of the steps, and of the other scales: a tile's barriers lie between
+    if (more) issue(then.t, scales + (flip ^ 1) * G::kScales);
+    v4f z[kNF][kMF];
+    G::scaled(scales + flip * G::kScales, wm, wn, lane, acc, z);
+    G::template finish<ACT>(a, at, wm, wn, lane, z);
+    if (!more) return;
+    whole = t.m0 + 256 <= t.mEnd && (GATED ? t.n0 / 2 + 128 <= t.O : t.n0 + 256 <= t.N);
+    at = then;
   }
 }
 
@@ -736,6 +914,16 @@ vrResult_t launch_tiles(GemmArgs& a, hipStream_t st) {
   });
 }
 
+template <int DT, int ACT, bool GATED>
+vrResult_t launch_run(GemmArgs& a, hipStream_t st) {
+  a.mt = a.counts ? a.rows / 256 + a.G : (a.rows + 255) / 256;
+  a.nt = GATED ? (a.O + 127) / 128 : (a.N + 255) / 256;
+  const uint64_t tiles = (uint64_t)a.R * a.mt * a.nt;
+  if (tiles > 0x7FFFFFFFull - 256) return VR_ERR_INVALID_ARGUMENT;
+  hipLaunchKernelGGL((k_gemm_run<DT, ACT, GATED>), dim3(256), dim3(512), 0, st, a, static_cast<int>(tiles));
+  return hipGetLastError() == hipSuccess ? VR_OK : VR_ERR_HIP;
+}
+
 // Tiles of size n x n to expect: a group's last row tile is half empty.
 template <int MODE, bool GATED>
 uint64_t expected_tiles(const GemmArgs& a, int n) {
@@ -761,8 +949,10 @@ vrResult_t launch_any(GemmArgs& a, hipStream_t st) {
   const uint64_t n128 = expected_tiles<MODE, GATED>(a, 128);
   if constexpr (DT != VR_DT_F32 && DIRECT) {
     const uint64_t n256 = expected_tiles<MODE, GATED>(a, 256);
-    if ((n256 + 255) / 256 * 100 <= (n128 + 511) / 512 * 59)
-      return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
+    if ((n256 + 255) / 256 * 100 <= (n128 + 511) / 512 * 59) {
+      if constexpr (kInt8<DT>) return launch_run<DT, ACT, GATED>(a, st);
+      else return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
+    }
   }
   if (n128 >= 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
   if constexpr (DIRECT) {
