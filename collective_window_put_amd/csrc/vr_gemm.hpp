@@ -843,6 +843,26 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
   for (int h = 0; h < NW; ++h)
 #pragma unroll
     for (int j = 0; j < MT; ++j) z[h][j] = Acc<DT>{0, 0, 0, 0};
+  // what the epilogue reads, in 8 bits, on its way with the weights: one latency less
+  const int m = tid >> 2, p = tid & 3;
+  [[maybe_unused]] float sx = 0.0f, sw[NW][4], bias[NW][4], res[4];
+  if constexpr (kInt8<DT>) {
+    constexpr int kOut = kOutOf<DT>;
+    if (m < rows) {
+      const int at = c0 + p * 4, n = a.O - at;
+      sx = *reinterpret_cast<const float*>(a.a.p[r] + (uint64_t)(first + m + 1) * a.lda - 4);
+#pragma unroll
+      for (int h = 0; h < NW; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t row = (uint64_t)g.g * a.N + h * a.O + min(at + j, a.O - 1);
+          sw[h][j] = *reinterpret_cast<const float*>(a.b.p[r] + (row + 1) * a.ldb - 4);
+        }
+        if (a.bias.p[r]) load4<kOut>(a.bias.p[r], (uint64_t)g.g * a.N + h * a.O + at, n, bias[h]);
+      }
+      if (a.residual.p[r]) load4<kOut>(a.residual.p[r], (uint64_t)(first + m) * a.O + at, n, res);
+    }
+  }
   const int per = (a.K + 8 * kStep - 1) / (8 * kStep) * kStep;
   stream_products<DT, NW, MT, U>(w, x, wave * per, min(a.K, (wave + 1) * per), a.K, z);
 #pragma unroll
@@ -850,7 +870,6 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
 #pragma unroll
     for (int j = 0; j < MT; ++j) part[wave][h][j * 16 + i][q] = z[h][j];
   __syncthreads();
-  const int m = tid >> 2, p = tid & 3;
   if (m >= rows) return;
   Acc<DT> s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
@@ -858,16 +877,22 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
 #pragma unroll
     for (int v = 0; v < 8; ++v) s[h] += part[v][h][m][p];
   if constexpr (kInt8<DT>) {
-    const float sx = *reinterpret_cast<const float*>(a.a.p[r] + (uint64_t)(first + m + 1) * a.lda - 4);
-    v4f y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    const int n = a.O - (c0 + p * 4);
+    if (n <= 0) return;
+    float y[4];
 #pragma unroll
-    for (int h = 0; h < NW; ++h)
+    for (int j = 0; j < 4; ++j) {
+      float z[NW];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint64_t row = (uint64_t)g.g * a.N + h * a.O + min(c0 + p * 4 + q, a.O - 1);
-        y[h][q] = static_cast<float>(s[h][q]) * sx * *reinterpret_cast<const float*>(a.b.p[r] + (row + 1) * a.ldb - 4);
+      for (int h = 0; h < NW; ++h) {
+        z[h] = static_cast<float>(s[h][j]) * sx * sw[h][j];
+        if (a.bias.p[r]) z[h] += bias[h][j];
       }
-    epilogue<kOutOf<DT>, ACT, GATED>(a, r, g.g, first + m, c0 + p * 4, y[0], y[1]);
+      y[j] = act_value<kOutOf<DT>, ACT>(z[0]);
+      if (GATED) y[j] *= z[NW - 1];
+      if (a.residual.p[r]) y[j] += res[j];
+    }
+    store4<kOutOf<DT>>(a.out.p[r], (uint64_t)(first + m) * a.O + c0 + p * 4, n, y);
   } else {
     epilogue<DT, ACT, GATED>(a, r, g.g, first + m, c0 + p * 4, s[0], s[1]);
   }
@@ -954,6 +979,13 @@ vrResult_t launch_any(GemmArgs& a, hipStream_t st) {
       else return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 256, 256, 128, 64, 2>(a, st);
     }
   }
+  // Experts of few rows each in 8 bits are bound by the weights' bytes: 64 x 128 tiles
+  // with three steps in the LDS take 83, 92, 94 us at 32, 128, 256 rows of 32
+  // experts on 8 ranks, 2048 -> 512 gated; 64 x 64 ones 86, 94, 96, 128 x 128 ones
+  // 94, 98, 100.
+  if constexpr (kInt8<DT> && DIRECT) {
+    if (a.G > 1 && a.rows / a.G < 64) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 64, 128, 32, 64, 3>(a, st);
+  }
   if (n128 >= 256) return launch_tiles<DT, MODE, ACT, GATED, DIRECT, 128, 128, 64, 64, 2>(a, st);
   if constexpr (DIRECT) {
     if (expected_tiles<MODE, GATED>(a, 64) <= 512)
@@ -968,7 +1000,12 @@ vrResult_t launch_gemm(GemmArgs& a, hipStream_t st) {
     // Few rows: against 64 x 64 tiles, us at 1, 32, 64 rows of bf16 4096 x 4096
     // weights 11, 15, 25 to 22; at 64, 256 rows of fp32 2048 x 2048 weights, whose
     // tiles are bound by the matrix units, 16, 47 to 45. Groups are ragged.
-    const int most = (DT == VR_DT_F32 ? 128 : 32) / (a.G > 1 ? 2 : 1), rows = a.rows / a.G;
+    // 8 bits: of a single group alone, at 32, 64 rows of 4096 x 4096 weights 10, 15 to
+    // 14.4, 14.5, at 64, 128 rows of 2048 x 2048 weights 7.2, 11 to 9.5, 9.6; by expert
+    // tiles are as fast from the first row on (8 x 32 rows of 32 experts, 2048 ->
+    // 512 gated: 98 to 83).
+    const int few8 = a.G > 1 ? -1 : (uint64_t)a.N * a.K <= 4u << 20 ? 64 : 32;
+    const int most = kInt8<DT> ? few8 : (DT == VR_DT_F32 ? 128 : 32) / (a.G > 1 ? 2 : 1), rows = a.rows / a.G;
     if (rows <= 16 && rows <= most) return launch_few<DT, ACT, GATED, 1>(a, st);
     if (rows <= most) return launch_few<DT, ACT, GATED, 2>(a, st);
   }
