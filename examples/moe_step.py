@@ -8,9 +8,14 @@ A training step over many tokens, forward
 
 and backward
 
-    vr_dispatch (of the output's gradient) -> vr_linear_backward (down, up) -> vr_combine -> vr_route_backward
+    vr_combine_backward -> vr_linear_backward (down, up) -> vr_combine -> vr_route_backward
 
-and a decoding step over a few tokens, vr_moe_layer, with the same weights.
+a decoding step over a few tokens, vr_moe_layer, with the same weights, and the
+layer as the block of a model has it: behind a root-mean-square norm that takes
+the residual stream along (vr_norm, vr_norm_backward), with the router's product,
+and served in 8 bits
+
+    vr_norm -> vr_linear, vr_route -> vr_dispatch -> vr_linear_q8 -> vr_quantize -> vr_linear_q8 -> vr_combine
 """
 from __future__ import annotations
 
@@ -98,17 +103,9 @@ class MoeStep:
     def backward(self):
         """dx, dw_up, dw_down and dlogits from dout, after forward."""
         c, R, K = self.win.comm, self.R, self.K
-        # dweights[s][t][k] = dout[s][t] . y of the entry's row; the row of an entry: its expert's rank and position
-        rank = (self.topk // (self.E // R)).clamp(min=0).long()
-        row = self.pos.clamp(min=0).long()
-        have = self.pos >= 0
-        mix = self.y[rank, row].float()  # [R, T, K, H]
-        dweights = torch.where(have, (mix * self.dout.float()[:, :, None]).sum(-1), 0.0)
-        # each row's gradient: its token's, times the row's weight
-        self._scatter(self._dout, self._dy)
-        scale = torch.zeros(R, self.rows, device="cuda")
-        scale[rank[have], row[have]] = self.weights[have]
-        self.dy.copy_(self.dy.float() * scale[..., None])
+        dweights = torch.empty_like(self.weights)
+        vr.vr_combine_backward(c, self._dout, self._y, self.rows, self.H * self.dtype.itemsize, DT[self.dtype], self.topk,
+                               self.weights, self.pos, self.T, K, self.E, dy=self._dy, dweights=dweights)
         vr.vr_linear_backward(c, self.down, self._dy, self._h, self._w_down, dx=self._dh, dw=self._dw_down,
                               group_rows=self.counts, **self.ws)
         vr.vr_linear_backward(c, self.up, self._dh, self._recv, self._w_up, preact=self._preact, dx=self._drecv,
@@ -141,6 +138,68 @@ class MoeStep:
         self.win.close()
 
 
+class MoeBlock(MoeStep):
+    """The layer behind a norm: stream = branch + residual, x = norm(stream) * gain, logits = x router^T, out = the layer's.
+    The next block adds out to stream. Weights are kept in 8 bits too, for serving."""
+
+    EPS = 1e-5
+
+    def __init__(self, R, T, H, I, E, K, dtype=torch.bfloat16):  # noqa: E741
+        super().__init__(R, T, H, I, E, K, dtype)
+        G, rows = E // R, self.rows
+        for name, shape in dict(branch=(T, H), residual=(T, H), stream=(T, H), gain=(H,), router=(1, E, H), dstream=(T, H),
+                                dx_router=(T, H), dbranch=(T, H), dgain=(H,), drouter=(1, E, H)).items():
+            t, s = self.win.tensor(shape, dtype)
+            setattr(self, name, t)
+            setattr(self, "_" + name, s)
+        self.row_h, self.row_i = vr.vr_q8_row_bytes(H), vr.vr_q8_row_bytes(I)
+        for name, shape in dict(x8=(T, self.row_h), recv8=(rows, self.row_h), h8=(rows, self.row_i),
+                                w_up8=(G * 2 * I, self.row_h), w_down8=(G * H, self.row_i)).items():
+            t, s = self.win.tensor(shape, torch.uint8)
+            setattr(self, name, t)
+            setattr(self, "_" + name, s)
+        self.norm = vr.vrNormShape(DT[dtype], T, H, self.EPS)
+        self.scores = vr.vrLinearShape(DT[dtype], T, 1, H, E, vr.VR_ACT_NONE)
+        need = max(vr.vr_norm_backward_workspace_bytes(R, self.norm), vr.vr_linear_backward_workspace_bytes(R, self.scores))
+        self.ws2 = dict(workspace=torch.empty(need, dtype=torch.uint8, device="cuda"), workspace_bytes=need)
+
+    def forward(self):
+        """out and stream from branch and residual."""
+        c = self.win.comm
+        vr.vr_norm(c, self.norm, self._branch, gain=self._gain, residual=self._residual, sum=self._stream, out=self._x)
+        vr.vr_linear(c, self.scores, self._x, self._router, self._logits)
+        super().forward()
+
+    def backward(self):
+        """The layer's gradients, and dbranch (residual's is the same), dgain and drouter, from dout and dstream."""
+        c = self.win.comm
+        super().backward()
+        vr.vr_linear_backward(c, self.scores, self._dlogits, self._x, self._router, dx=self._dx_router, dw=self._drouter,
+                              **self.ws2)
+        self.dx.add_(self.dx_router)
+        vr.vr_norm_backward(c, self.norm, self._dx, self._stream, gain=self._gain, dsum=self._dstream, dh=self._dbranch,
+                            dgain=self._dgain, **self.ws2)
+
+    def quantize_weights(self):
+        c, dt, G = self.win.comm, DT[self.dtype], self.E // self.R
+        vr.vr_quantize(c, self._w_up, dt, G * 2 * self.I, self.H, self._w_up8)
+        vr.vr_quantize(c, self._w_down, dt, G * self.H, self.I, self._w_down8)
+
+    def serve(self):
+        """out and stream in 8 bits: half the dispatch's bytes and the experts' weights'."""
+        c, dt = self.win.comm, DT[self.dtype]
+        vr.vr_norm(c, self.norm, self._branch, gain=self._gain, residual=self._residual, sum=self._stream, out=self._x,
+                   q8=self._x8)
+        vr.vr_linear(c, self.scores, self._x, self._router, self._logits)
+        vr.vr_route(c, self._logits, dt, self.T, self.K, self.E, self.topk, self.weights, vr.VR_ROUTE_RENORM)
+        vr.vr_dispatch(c, self._x8.window, 0, self.row_h, self.topk, self.T, self.K, self.E, self._recv8.window, 0, self.rows,
+                       self.counts, self.src, self.pos, 0, 1)
+        vr.vr_linear_q8(c, self.up, self._recv8, self._w_up8, self._h, group_rows=self.counts)
+        vr.vr_quantize(c, self._h, dt, self.rows, self.I, self._h8, groups=self.E // self.R, group_rows=self.counts)
+        vr.vr_linear_q8(c, self.down, self._h8, self._w_down8, self._y, group_rows=self.counts)
+        self._gather(self._y, self.weights, self._out)
+
+
 def main():
     gen = torch.Generator(device="cuda").manual_seed(0)
     R, T, H, I, E, K = 8, 512, 1024, 512, 64, 8  # noqa: E741
@@ -159,6 +218,21 @@ def main():
     print("training step: out", tuple(step.out.shape), "rms", float(step.out.float().square().mean().sqrt()))
     print("decoding step: out", tuple(few.shape), "rms", float(few.float().square().mean().sqrt()))
     step.close()
+
+    block = MoeBlock(R, T, H, I, E, K)
+    fill(block.branch), fill(block.residual), fill(block.dout), fill(block.dstream)
+    fill(block.w_up, H ** -0.5), fill(block.w_down, I ** -0.5), fill(block.router, H ** -0.5)
+    block.gain.fill_(1.0)
+    block.forward()
+    block.backward()
+    block.check()
+    whole = block.out.float().clone()
+    print("block: out rms", float(whole.square().mean().sqrt()), "dgain rms", float(block.dgain.float().square().mean().sqrt()))
+    block.quantize_weights()
+    block.serve()
+    block.check()
+    print("block in 8 bits: off by", float((block.out.float() - whole).norm() / whole.norm()))
+    block.close()
 
 
 if __name__ == "__main__":
