@@ -76,6 +76,39 @@ def test_calls_larger_than_the_caches(rows, cols):
         job.assert_no_async_error()
 
 
+@pytest.mark.parametrize("R,rows,cols,dtype", [(8, 2048, 2048, "bf16"), (3, 5462, 1100, "bf16"), (1, 16384, 1023, "f32"),
+                                               (8, 4099, 1024, "f32")])
+def test_norm_gradients_of_many_rows(R, rows, cols, dtype):
+    # dh in dsum's place, also where a row's last 16 bytes are two lanes' (cols no multiple of them)
+    import torch
+    say(f"norm gradients of many rows: {R} x {rows} x {cols} {dtype}")
+    dt, half = (torch.bfloat16, BF) if dtype == "bf16" else (torch.float32, STEP)
+    shape = vr.vrNormShape(vr.VR_DT_BF16 if dtype == "bf16" else vr.VR_DT_F32, rows, cols, 1e-5)
+    with Job(R) as job:
+        h, hs = _window(job, (rows, cols), dt, 1)
+        gain, gs = _window(job, (cols,), dt, 20)
+        dout, ds = _window(job, (rows, cols), dt, 40)
+        dsum, ss = _window(job, (rows, cols), dt, 60)
+        dg, dgs = _window(job, (cols,), dt)
+        before = [t.double() for t in dsum]
+        need = vr.vr_norm_backward_workspace_bytes(R, shape)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        vr.vr_norm_backward(job.comm, shape, ds, hs, gain=gs, dsum=ss, dh=ss, dgain=dgs, workspace=ws, workspace_bytes=need)
+        torch.cuda.synchronize()
+        rel = (cols + 4) * STEP / 2 + 8 * STEP
+        for r in range(R):
+            v, d = h[r].double(), dout[r].double()
+            root = (v.square().mean(-1, keepdim=True) + 1e-5).sqrt()
+            n, w = v / root, d * gain[r].double()
+            want = before[r] + (w - n * (w * n).mean(-1, keepdim=True)) / root
+            tol = (w.abs() * (rel + 8 * STEP) + n.abs() * (w * n).abs().mean(-1, keepdim=True)
+                   * ((cols + 4) * STEP + 2 * rel + 8 * STEP)) / root
+            assert bool(((dsum[r].double() - want).abs() <= tol + want.abs() * (half + 2 * STEP) + 2.0 ** -130).all())
+            wg = (d * n).sum(0)
+            assert bool(((dg[r].double() - wg).abs() <= (d * n).abs().sum(0) * ((rows + 8) * STEP + rel) + wg.abs() * half).all())
+        job.assert_no_async_error()
+
+
 def test_more_rows_than_a_launch_has_workgroups():
     # 2^21 workgroups of a row each, and three rows more; 8.8 GB of values
     import torch
