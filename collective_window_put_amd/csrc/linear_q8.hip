@@ -2,7 +2,12 @@
 // (vr_linear_q8): out = act(z) (gated: act(z_g) * z_u) + residual with
 //   z[m][n] = (sum over k of x[m][k] w[n][k]) * scale of x's row m * scale of
 //             w's row n + bias[n]
-// The sums are 32-bit integers, exact; they become binary32 once, at the end.
+// The sums are 32-bit integers, exact; they become binary32 once, at the end. The
+// tiles and the kernels for few rows are those of vr_linear, with matrix
+// instructions of twice the rate and half the bytes of bf16; large calls take
+// k_gemm_run. 8192 x 4096 x 4096 with gelu, bias and residual: 149 us, 1.84 POP/s
+// (bf16: 303 us); 8 x 32768 rows (15/16 used) by 32 experts,
+// 512 -> 512 gated: 244 us, 1.06 POP/s.
 #include <hip/hip_runtime.h>
 
 #include "vr_gemm.hpp"

@@ -1,5 +1,6 @@
 // Shared by the layer kernels (route.hip, linear.hip, linear_q8.hip, moe_layer.hip,
-// norm.hip, combine_grad.hip): element traits, activations, wave reductions and the row ranges of groups.
+// norm.hip, combine_grad.hip): element traits, activations, wave reductions and
+// the row ranges of groups.
 #pragma once
 
 #include <hip/hip_runtime.h>
