@@ -1460,7 +1460,8 @@ static vrResult_t rows_in_8_bits(vrComm_t c, const vrSlice& x, int dtype, int ro
   const SliceUse use[] = {{&x, n, back}, {&q8, n8, !back, kQ8Align}};
   const vrResult_t r = check_slices(c, use, 2, es, nullptr, nullptr);
   if (r != VR_OK) return r;
-  if (group_rows && (!dev_span_ok(c, group_rows, counts) || !clear_of(c, group_rows, counts, back ? x : q8, back ? n : n8)))
+  if (group_rows && (reinterpret_cast<uintptr_t>(group_rows) % 4 || !dev_span_ok(c, group_rows, counts) ||
+                     !clear_of(c, group_rows, counts, back ? x : q8, back ? n : n8)))
     return VR_ERR_INVALID_ARGUMENT;
   if (!rows) return VR_OK;
   return back ? launch_dequantize(c, q8, dtype, rows, cols, groups, group_rows, x, S(stream))
@@ -1484,6 +1485,7 @@ vrResult_t vr_linear_q8(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w
   if (!x.window || !w.window || !out.window) return VR_ERR_INVALID_ARGUMENT;
   const LinearBytes b(c->nranks, *s);
   const size_t row = q8_row_bytes(s->in), n = (size_t)s->out * ((s->act & VR_ACT_GATED) ? 2 : 1);
+  if (group_rows && reinterpret_cast<uintptr_t>(group_rows) % 4) return VR_ERR_INVALID_ARGUMENT;
   const SliceUse use[] = {{&x, row * s->rows, false, kQ8Align}, {&w, row * s->groups * n, false, kQ8Align},
                           {&bias, b.bias, false},               {&residual, b.out, false},
                           {&out, b.out, true}};

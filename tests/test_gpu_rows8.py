@@ -148,3 +148,21 @@ def test_refusals():
             call(groups=3, group_rows=counts)()
             call()()
         job.assert_no_async_error()
+
+
+def test_counts_at_odd_addresses():
+    import torch
+    say("rows in 8 bits, their product: counts that are no 32-bit words of memory")
+    R, rows, cols = 2, 6, 24
+    with Job(R) as job:
+        x = Tensors(job, "f32").put(shape=(rows, cols))[0]
+        q8, _ = q8_window(job, (rows, row_bytes(cols)))
+        w, _ = q8_window(job, (cols, row_bytes(cols)))
+        counts = torch.zeros(R + 1, dtype=torch.int32, device="cuda")
+        shape = vr.vrLinearShape(vr.VR_DT_F32, rows, 1, cols, cols, 0)
+        for off in (1, 2, 3):
+            at = counts.data_ptr() + off
+            refused(lambda: vr.vr_quantize(job.comm, x, vr.VR_DT_F32, rows, cols, q8, group_rows=at))
+            refused(lambda: vr.vr_dequantize(job.comm, q8, vr.VR_DT_F32, rows, cols, x, group_rows=at))
+            refused(lambda: vr.vr_linear_q8(job.comm, shape, q8, w, x, group_rows=at))
+        job.assert_no_async_error()
