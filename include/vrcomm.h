@@ -727,9 +727,10 @@ vrResult_t vr_moe_layer(vrComm_t comm, const vrMoeShape* shape, vrSlice x, const
  * together. Slices of q8 rows start at a multiple of 4 bytes (of 16: fastest).
  * A row becomes one like this: m its largest magnitude, scale = m / 127, value =
  * x * (127 / m) rounded to nearest even, each off by at most half a scale (and the
- * binary32 roundings of the two quotients and the product). A row with m below 2^-119 (its scale would be subnormal) gets scale 0 and zeros. A
- * row with a NaN or an infinity gets scale NaN and zeros, so that everything
- * computed from it is NaN, and sets VR_ASYNC_BAD_VALUE. */
+ * binary32 roundings of the two quotients and the product). A row with m below
+ * 2^-119 (its scale would be subnormal) gets scale 0 and zeros. A row with a NaN
+ * or an infinity gets scale NaN and zeros, so that everything computed from it is
+ * NaN, and sets VR_ASYNC_BAD_VALUE. */
 
 /* (cols + 4) rounded up to a multiple of 128; 0 unless cols is in 1..2^20. */
 size_t vr_q8_row_bytes(int cols);
