@@ -213,10 +213,11 @@ __device__ inline void store_piece(char* row, int col, int cols, const float* f)
   }
 }
 
-// 1 / sqrt(ss / cols + eps)
-__device__ inline float inverse_root(float ss, int cols, float eps) { return 1.0f / sqrtf(ss / static_cast<float>(cols) + eps); }
-// What a row whose squares pass binary32 is multiplied by before they are
-// taken: a power of two that brings its largest magnitude (bits m, finite) to
+// The square of a row's root, and 1 / root.
+__device__ inline float root_square(float ss, int cols, float eps) { return ss / static_cast<float>(cols) + eps; }
+__device__ inline float inverse_root(float ss, int cols, float eps) { return 1.0f / sqrtf(root_square(ss, cols, eps)); }
+// What a row whose squares, or the root's square, pass binary32 is multiplied by
+// before they are taken: a power of two that brings its largest magnitude (bits m, finite) to
 // [1, 2). *bad: m is no number, and the root is infinite or NaN.
 __device__ inline float down(uint32_t m, bool* bad) {
   *bad = m >= kInfBits;
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_rows(const RowArgs a) {
       // only here: sum may lie where residual does, and where two threads share columns both have read them now
       if (a.sum.p[r]) each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_once<DT, MODE>(a.sum.p[r] + at, col, h[p]); });
       float inv = inverse_root(ss, cols, a.eps);
-      if (!(ss < INFINITY)) {  // the same in all of the row's threads
+      if (!(root_square(ss, cols, a.eps) < INFINITY)) {  // the same in all of the row's threads
         uint32_t m = 0;
         each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(h[p][j])); });
         m = row_reduce<TPR>(m, red_max[flip], Max());
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rows_long(const RowArgs a) {
       ss = row_reduce<T>(ss, red_sum, Add());
       inv = inverse_root(ss, a.cols, a.eps);
       __syncthreads();
-      if (!(ss < INFINITY)) {
+      if (!(root_square(ss, a.cols, a.eps) < INFINITY)) {
         uint32_t m = 0;
         for (int col = t * kC; col < a.cols; col += T * kC) {
           float h[kC];
@@ -553,7 +554,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const BackArgs a)
       }
     };
     sums();
-    if (!(ss < INFINITY)) {
+    if (!(root_square(ss, cols, a.eps) < INFINITY)) {
       uint32_t m = 0;
       each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(piece_f32<DT>(hv[p], j))); });
       m = row_reduce<TPR>(m, red_max, Max());
@@ -642,7 +643,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs 
       __syncthreads();
     };
     sums();
-    if (!(ss < INFINITY)) {
+    if (!(root_square(ss, a.cols, a.eps) < INFINITY)) {
       uint32_t m = 0;
       for (int col = t * kC; col < a.cols; col += T * kC) {
         float h[kC];
