@@ -223,6 +223,20 @@ __device__ inline float down(uint32_t m, bool* bad) {
   *bad = m >= kInfBits;
   return ldexpf(1.0f, 127 - static_cast<int>(m >> 23));
 }
+// A gradient's row is taken again where the root's square is no binary32 number, or
+// the mean of g n is so large that its product with an n (2^10 at most, the root of
+// the most columns) might not be one: h is then brought below 2 and g below 2^65, where
+// they are not, by powers of two. Sums of 2^20 products of those stay inside binary32.
+constexpr float kMostMean = 0x1p117f;
+__device__ inline bool again_scaled(float square, float mean) { return !(square < INFINITY && fabsf(mean) < kMostMean); }
+struct Scales {
+  float h, g, back;  // back = h / g, what brings the scaled row's gradient back
+  bool bad;          // a value of h is no number, and the root is infinite or NaN
+};
+__device__ inline Scales scales_of(uint32_t mh, uint32_t mg) {  // largest magnitudes, as bits
+  const int eh = max(static_cast<int>(mh >> 23) - 127, 0), eg = mg < kInfBits ? max(static_cast<int>(mg >> 23) - 191, 0) : 0;
+  return {ldexpf(1.0f, -eh), ldexpf(1.0f, -eg), ldexpf(1.0f, eg - eh), mh >= kInfBits};
+}
 
 // Threads of a workgroup whose rows take TPR.
 constexpr int threads_of(int tpr) { return tpr == 64 ? 256 : tpr; }
@@ -492,11 +506,14 @@ struct BackArgs {
 // row of sums per row another pass over the data. Three rows are read for one that
 // is written: 8 x 2048 rows of 4096 bf16 with dsum and dgain 98 us, 5.5 TB/s (other
 // threads to a row and 512 to 2048 slots: 98 to 104).
+// The least waves to a SIMD that its registers have to leave room for: 64 of them let two workgroups of 16 waves onto a
+// compute unit, which the compiler misses by five (2000 rows of 4096 fp32: 25.4 us, else 27.4); the other modes would spill.
+template <int DT, int TPR, int P, int MODE> constexpr int kBackWaves = DT == VR_DT_F32 && TPR == 1024 && P == 1 && MODE == kWhole ? 8 : 1;
 template <int DT, int TPR, int P, int MODE>
-__global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const BackArgs a) {
+__global__ __launch_bounds__(threads_of(TPR), (kBackWaves<DT, TPR, P, MODE>)) void k_norm_back(const BackArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = threads_of(TPR) / TPR, kW = TPR / 64;
   __shared__ float red[2][2][kW];
-  __shared__ uint32_t red_max[kW];
+  __shared__ uint32_t red_max[2][kW];
   const int r = blockIdx.y, t = threadIdx.x % TPR, cols = a.cols;
   const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const bool gained = a.gain.p[r] != nullptr, more = a.dsum.p[r] != nullptr;
@@ -528,13 +545,17 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const BackArgs a)
       for (int p = 0; p < P; ++p)
         if (more) asm volatile("" : "+v"(sv[p]));
     }
-    float by = 1.0f, ss = 0.0f, sg = 0.0f;
+    float by = 1.0f, gby = 1.0f, back = 1.0f, ss = 0.0f, sg = 0.0f;
+    const auto weighted = [&](int p, int j) {
+      const float d = piece_f32<DT>(dv[p], j);
+      return gained ? d * piece_f32<DT>(gv[p], j) : d;
+    };
     const auto sums = [&] {
       ss = sg = 0.0f;
       each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) {
-        const float h = piece_f32<DT>(hv[p], j) * by, d = piece_f32<DT>(dv[p], j);
+        const float h = piece_f32<DT>(hv[p], j) * by;
         ss = fmaf(h, h, ss);
-        sg = fmaf(gained ? d * piece_f32<DT>(gv[p], j) : d, h, sg);
+        sg = fmaf(weighted(p, j) * gby, h, sg);
       });
       ss = wave_sum(ss);
       sg = wave_sum(sg);
@@ -553,28 +574,44 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const BackArgs a)
         }
       }
     };
+    const auto mean_gn = [&](float inv) { return sg * inv / static_cast<float>(cols); };
     sums();
-    if (!(root_square(ss, cols, a.eps) < INFINITY)) {
-      uint32_t m = 0;
-      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) { m = max(m, magnitude(piece_f32<DT>(hv[p], j))); });
-      m = row_reduce<TPR>(m, red_max, Max());
+    float inv = inverse_root(ss, cols, a.eps), mean = mean_gn(inv);
+    if (again_scaled(root_square(ss, cols, a.eps), mean)) {
+      // here and below, as if read anew: the compiler keeps widened values across this seldom way otherwise, and of bf16 spills one
+      if constexpr (TPR == 1024 && P == 2) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) asm volatile("" : "+v"(dv[p]));
+      }
+      uint32_t mh = 0, mg = 0;
+      each<DT, TPR, P, MODE != kAny>(t, cols, [&](int p, int j) {
+        mh = max(mh, magnitude(piece_f32<DT>(hv[p], j)));
+        mg = max(mg, magnitude(weighted(p, j)));
+      });
+      mh = row_reduce<TPR>(mh, red_max[0], Max());
+      mg = row_reduce<TPR>(mg, red_max[1], Max());
       if (TPR > 64) __syncthreads();  // red is written again, and red_max by the next such row
-      bool bad;
-      const float f = down(m, &bad);
-      if (!bad) {
-        by = f;
+      const Scales f = scales_of(mh, mg);
+      if (!f.bad) {
+        by = f.h;
+        gby = f.g;
+        back = f.back;
         sums();
+        inv = inverse_root(ss, cols, a.eps * by * by);
+        mean = mean_gn(inv);
+      }
+      if constexpr (TPR == 1024 && P == 2) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) asm volatile("" : "+v"(dv[p]));
       }
     }
-    const float inv = inverse_root(ss, cols, a.eps * by * by);
-    const float mean = sg * inv / static_cast<float>(cols);  // of g n
     each_piece<DT, TPR, P>(t, cols, [&](int p, int col) {
       float v[kC];
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         const float n = piece_f32<DT>(hv[p], j) * by * inv, d = piece_f32<DT>(dv[p], j);
         acc[p][j] = fmaf(d, n, acc[p][j]);
-        v[j] = ((gained ? d * piece_f32<DT>(gv[p], j) : d) - n * mean) * inv * by;
+        v[j] = (weighted(p, j) * gby - n * mean) * inv * back;
         if (more) v[j] += piece_f32<DT>(sv[p], j);
       }
       if (a.dh.p[r]) store_once<DT, MODE>(a.dh.p[r] + at, col, v);
@@ -609,7 +646,7 @@ template <int DT>
 __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, T = kLongThreads;
   __shared__ float red[2][T / 64];
-  __shared__ uint32_t red_max[T / 64];
+  __shared__ uint32_t red_max[2][T / 64];
   const int r = blockIdx.y, t = threadIdx.x;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const uint64_t at = (uint64_t)row * a.cols * kES;
@@ -625,7 +662,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs 
 #pragma unroll
       for (int j = 0; j < kC; ++j) g[j] *= f[j];
     };
-    float by = 1.0f, ss, sg;
+    float by = 1.0f, gby = 1.0f, back = 1.0f, ss, sg;
     const auto sums = [&] {
       ss = sg = 0.0f;
       for (int col = t * kC; col < a.cols; col += T * kC) {
@@ -635,33 +672,41 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs 
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
           ss = fmaf(h[j] * by, h[j] * by, ss);
-          sg = fmaf(g[j], h[j] * by, sg);
+          sg = fmaf(g[j] * gby, h[j] * by, sg);
         }
       }
       ss = row_reduce<T>(ss, red[0], Add());
       sg = row_reduce<T>(sg, red[1], Add());
       __syncthreads();
     };
+    const auto mean_gn = [&](float inv) { return sg * inv / static_cast<float>(a.cols); };
     sums();
-    if (!(root_square(ss, a.cols, a.eps) < INFINITY)) {
-      uint32_t m = 0;
+    float inv = inverse_root(ss, a.cols, a.eps), mean = mean_gn(inv);
+    if (again_scaled(root_square(ss, a.cols, a.eps), mean)) {
+      uint32_t mh = 0, mg = 0;
       for (int col = t * kC; col < a.cols; col += T * kC) {
-        float h[kC];
+        float h[kC], g[kC];
         get(a.h.p[r], at, col, h);
+        weighted(col, g);
 #pragma unroll
-        for (int j = 0; j < kC; ++j) m = max(m, magnitude(h[j]));
+        for (int j = 0; j < kC; ++j) {
+          mh = max(mh, magnitude(h[j]));
+          mg = max(mg, magnitude(g[j]));
+        }
       }
-      m = row_reduce<T>(m, red_max, Max());
+      mh = row_reduce<T>(mh, red_max[0], Max());
+      mg = row_reduce<T>(mg, red_max[1], Max());
       __syncthreads();
-      bool bad;
-      const float f = down(m, &bad);
-      if (!bad) {
-        by = f;
+      const Scales f = scales_of(mh, mg);
+      if (!f.bad) {
+        by = f.h;
+        gby = f.g;
+        back = f.back;
         sums();
+        inv = inverse_root(ss, a.cols, a.eps * by * by);
+        mean = mean_gn(inv);
       }
     }
-    const float inv = inverse_root(ss, a.cols, a.eps * by * by);
-    const float mean = sg * inv / static_cast<float>(a.cols);
     if (t == 0 && a.roots) {
       a.roots[((uint64_t)r * a.rows + row) * 2] = by;
       a.roots[((uint64_t)r * a.rows + row) * 2 + 1] = inv;
@@ -674,7 +719,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs 
       if (a.dsum.p[r]) get(a.dsum.p[r], at, col, s);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const float n = h[j] * by * inv, v = (g[j] - n * mean) * inv * by;
+        const float n = h[j] * by * inv, v = (g[j] * gby - n * mean) * inv * back;
         g[j] = a.dsum.p[r] ? v + s[j] : v;
       }
       store_piece<DT>(a.dh.p[r] + at, col, a.cols, g);

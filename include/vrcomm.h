@@ -763,7 +763,9 @@ vrResult_t vr_norm(vrComm_t comm, const vrNormShape* shape, vrSlice x, vrSlice r
  *   n = h / r, g = dout * gain: the gradient of x and of residual alike; may be
  *   dsum's own slice
  *   dgain [cols] = sum over the rank's rows of dout * n (zeros without rows)
- * At least one of the two is wanted. Sums run in a fixed order. */
+ * At least one of the two is wanted. Sums run in a fixed order. Squares and
+ * products that pass binary32 are taken again, scaled: where h and g are finite,
+ * dh is as the formula has it. */
 size_t vr_norm_backward_workspace_bytes(int nranks, const vrNormShape* shape);
 vrResult_t vr_norm_backward(vrComm_t comm, const vrNormShape* shape, vrSlice dout, vrSlice h, vrSlice gain,
                             vrSlice dsum, vrSlice dh, vrSlice dgain, void* workspace, size_t workspace_bytes,
