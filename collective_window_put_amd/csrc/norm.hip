@@ -97,14 +97,14 @@ __device__ inline uint32_t bytes4(const float* f, const To8& q) {
 }
 
 // The N = 4 or 8 values of columns [col, col + N) of a q8 row; the last n of
-// the row's values.
-template <int N>
+// the row's values. ALIGN: of col, in bytes (rows start on words).
+template <int N, int ALIGN>
 __device__ inline void store_bytes(char* row, int col, int n, const float* f, const To8& q) {
   uint32_t w[N / 4];
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) w[i] = bytes4(f + 4 * i, q);
   if (n >= N) {
-    __builtin_memcpy(__builtin_assume_aligned(row + col, 4), w, N);
+    __builtin_memcpy(__builtin_assume_aligned(row + col, ALIGN), w, N);
   } else {
 #pragma unroll
     for (int j = 0; j < N - 1; ++j)
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_rows(const RowArgs a) {
       const To8 q = to_8(m);
       if (m >= kInfBits && t == 0) atomic_or_u32(a.err, VR_ASYNC_BAD_VALUE);
       char* to = a.q8.p[r] + (uint64_t)row * a.row8;
-      each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_bytes<kC>(to, col, kC, h[p], q); });
+      each_piece<DT, TPR, P>(t, cols, [&](int p, int col) { store_bytes<kC, MODE == kAny ? 1 : 4>(to, col, kC, h[p], q); });
       store_scale(to, cols, a.row8, t, q);
     }
   }
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rows_long(const RowArgs a) {
       float y[kC];
       value(col, y);
       if (NORM && a.out.p[r]) store_piece<DT>(a.out.p[r] + at, col, a.cols, y);
-      if (quant) store_bytes<kC>(to, col, a.cols - col, y, q);
+      if (quant) store_bytes<kC, 4>(to, col, a.cols - col, y, q);
     }
     if (quant) store_scale(to, a.cols, a.row8, t, q);
     __syncthreads();  // red_max is read until here
