@@ -1225,6 +1225,10 @@ static bool workspace_ok(vrComm* c, const void* ws, size_t have, size_t need) {
   if (!need) return true;
   return ws && have >= need && reinterpret_cast<uintptr_t>(ws) % 256 == 0 && dev_span_ok(c, ws, need);
 }
+// n bytes of device memory that are 32-bit words.
+static bool words_ok(vrComm* c, const void* p, size_t n) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && dev_span_ok(c, p, n);
+}
 // Whether a device array lies clear of every rank's part of a slice.
 static bool clear_of(vrComm* c, const void* p, size_t n, const vrSlice& s, size_t sn) {
   if (!p || !s.window) return true;
@@ -1315,7 +1319,7 @@ vrResult_t vr_linear(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w, v
                           {&residual, b.out, false}, {&out, b.out, true}, {&preact, b.z, true}};
   vrResult_t r = check_slices(c, use, 6, b.es, &residual, &out);
   if (r != VR_OK) return r;
-  if (group_rows && (!dev_span_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out) ||
+  if (group_rows && (!words_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out) ||
                      !clear_of(c, group_rows, b.counts, preact, b.z)))
     return VR_ERR_INVALID_ARGUMENT;
   if (!s->rows) return VR_OK;
@@ -1336,7 +1340,7 @@ vrResult_t vr_linear_backward(vrComm_t c, const vrLinearShape* s, vrSlice dout, 
                           {&dx, b.x, true},      {&dw, b.w, true}, {&dbias, b.bias, true}};
   vrResult_t r = check_slices(c, use, 7, b.es, nullptr, nullptr);
   if (r != VR_OK) return r;
-  if (group_rows && !dev_span_ok(c, group_rows, b.counts)) return VR_ERR_INVALID_ARGUMENT;
+  if (group_rows && !words_ok(c, group_rows, b.counts)) return VR_ERR_INVALID_ARGUMENT;
   const size_t need = linear_backward_workspace_bytes(c->nranks, *s);
   if (!workspace_ok(c, ws, ws_bytes, need)) return VR_ERR_INVALID_ARGUMENT;
   if (group_rows &&
@@ -1460,7 +1464,7 @@ static vrResult_t rows_in_8_bits(vrComm_t c, const vrSlice& x, int dtype, int ro
   const SliceUse use[] = {{&x, n, back}, {&q8, n8, !back, kQ8Align}};
   const vrResult_t r = check_slices(c, use, 2, es, nullptr, nullptr);
   if (r != VR_OK) return r;
-  if (group_rows && (reinterpret_cast<uintptr_t>(group_rows) % 4 || !dev_span_ok(c, group_rows, counts) ||
+  if (group_rows && (!words_ok(c, group_rows, counts) ||
                      !clear_of(c, group_rows, counts, back ? x : q8, back ? n : n8)))
     return VR_ERR_INVALID_ARGUMENT;
   if (!rows) return VR_OK;
@@ -1485,13 +1489,12 @@ vrResult_t vr_linear_q8(vrComm_t c, const vrLinearShape* s, vrSlice x, vrSlice w
   if (!x.window || !w.window || !out.window) return VR_ERR_INVALID_ARGUMENT;
   const LinearBytes b(c->nranks, *s);
   const size_t row = q8_row_bytes(s->in), n = (size_t)s->out * ((s->act & VR_ACT_GATED) ? 2 : 1);
-  if (group_rows && reinterpret_cast<uintptr_t>(group_rows) % 4) return VR_ERR_INVALID_ARGUMENT;
   const SliceUse use[] = {{&x, row * s->rows, false, kQ8Align}, {&w, row * s->groups * n, false, kQ8Align},
                           {&bias, b.bias, false},               {&residual, b.out, false},
                           {&out, b.out, true}};
   const vrResult_t r = check_slices(c, use, 5, b.es, &residual, &out);
   if (r != VR_OK) return r;
-  if (group_rows && (!dev_span_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out)))
+  if (group_rows && (!words_ok(c, group_rows, b.counts) || !clear_of(c, group_rows, b.counts, out, b.out)))
     return VR_ERR_INVALID_ARGUMENT;
   if (!s->rows) return VR_OK;
   return launch_linear_q8(c, *s, x, w, bias, residual, group_rows, out, S(stream));
@@ -1519,7 +1522,7 @@ vrResult_t vr_combine_backward(vrComm_t c, vrSlice dout, vrSlice y, size_t cap, 
   } arr[] = {{topk, false}, {weights, false}, {send_pos, false}, {dweights, true}};
   for (int i = 0; i < 4; ++i) {
     if (i == 3 && !dweights) break;
-    if (reinterpret_cast<uintptr_t>(arr[i].p) % 4 || !dev_span_ok(c, arr[i].p, m)) return VR_ERR_INVALID_ARGUMENT;
+    if (!words_ok(c, arr[i].p, m)) return VR_ERR_INVALID_ARGUMENT;
     for (const SliceUse& u : use)
       if ((u.written || arr[i].written) && !clear_of(c, arr[i].p, m, *u.s, u.n)) return VR_ERR_INVALID_ARGUMENT;
     for (int j = 0; j < i; ++j)
