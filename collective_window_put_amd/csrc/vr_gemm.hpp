@@ -152,22 +152,36 @@ __device__ inline v4f from_raw4(typename Raw4<DT>::T v) {
   else return v4f{bf16lo(v[0]), bf16hi(v[0]), bf16lo(v[1]), bf16hi(v[1])};
 }
 
+// sum * scale of the row * scale of the channel. A sum, below 2^31, times a scale above
+// 2^64 might pass binary32 where a small second scale brings it back: such a scale
+// is taken in two parts.
+struct RowScale {
+  float s, after;
+  bool large;
+  __device__ explicit RowScale(float scale) : large(fabsf(scale) > 0x1p64f) {
+    s = large ? scale * 0x1p-64f : scale;
+    after = large ? 0x1p64f : 1.0f;
+  }
+  __device__ float operator()(int sum, float w) const { return static_cast<float>(sum) * s * w * after; }
+};
+
 // Epilogue of a wave's part of a tile that has all its columns: NF x MF
 // fragments from column c0 and row m0 (of the group; rows up to mEnd). Loads
 // are issued many rows ahead: out might be residual's own slice, so the
 // compiler keeps their order, and a fragment at a time each load's latency was
 // waited for in turn (82 of the 300 us of a dense 8192 x 4096 x 4096
 // product).
+// large: rows' second parts of scales are left, their scales in the LDS at row_scales.
 // PAIRS: fragments 2 p and 2 p + 1 hold the columns 32 p + 8 q + 0..3 and + 4..7 of
 // lane quarter q, not 16 each: 16-byte stores of bf16 rather than 8.
-// BARE: no bias, residual or preact. A tensor that may be absent costs a branch at
+// BARE: no bias, residual, preact or large scale. A tensor that may be absent costs a branch at
 // every use, and where the branches meet a wait for loads that were not issued,
 // which then waits for the stores and for the next tile's loads: the experts'
 // 8 x 32768 rows (15/16 used), 512 -> 512 gated, in 8 bits 302 to 275 us, in bf16 from 256
 // elements 271 to 257.
 template <int DT, int ACT, bool GATED, int NF, int MF, bool PAIRS, bool BARE>
 __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0, int m0, int mEnd, int c0, int lane,
-                                      const v4f (*acc)[MF]) {
+                                      v4f (*acc)[MF], [[maybe_unused]] bool large, [[maybe_unused]] const float* row_scales) {
   constexpr int kES = Elem<DT>::kSize, NO = GATED ? NF / 2 : NF, S = GATED ? 2 : 1;
   const int m1 = m0 + (lane & 15), col = c0 + (lane >> 4) * (PAIRS ? 8 : 4);
   const auto off = [](int i) { return PAIRS ? (i >> 1) * 32 + (i & 1) * 4 : i * 16; };
@@ -197,6 +211,11 @@ __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0,
 #pragma unroll
     for (int v = 0; v < kRows; ++v) {
       const uint64_t row = row0 + m1 + (j0 + v) * 16;
+      if (!BARE && large) {
+        const float after = RowScale(row_scales[(j0 + v) * 16 + (lane & 15)]).after;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) acc[i][j0 + v] *= after;
+      }
       if (m1 + (j0 + v) * 16 < mEnd) {
         float pair[8];
 #pragma unroll
@@ -347,15 +366,16 @@ struct Gemm {
   }
 
   template <int ACT>
-  __device__ static __forceinline__ void finish(const GemmArgs& a, const Spot& s, int wm, int wn, int lane, const v4f (*acc)[kMF]) {
+  __device__ static __forceinline__ void finish(const GemmArgs& a, const Spot& s, int wm, int wn, int lane, v4f (*acc)[kMF],
+                                                bool large = false, const float* row_scales = nullptr) {
     const Where& t = s.t;
     if constexpr (MODE == kFwd) {
       if (GATED ? t.n0 / 2 + BN / 2 <= a.O : t.n0 + BN <= a.N) {
         const int c0 = GATED ? (t.n0 + wn) / 2 : t.n0 + wn;
-        if (a.bias.p[s.r] || a.residual.p[s.r] || a.preact.p[s.r])
-          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, false>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc);
+        if (a.bias.p[s.r] || a.residual.p[s.r] || a.preact.p[s.r] || large)
+          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, false>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc, large, row_scales);
         else
-          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, true>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc);
+          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, true>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc, large, row_scales);
         return;
       }
     }
@@ -364,6 +384,11 @@ struct Gemm {
     for (int j = 0; j < kMF; ++j) {
       const int m = t.m0 + wm + j * 16 + (lane & 15);
       if (m >= t.mEnd) continue;
+      if (large) {
+        const float after = RowScale(row_scales[j * 16 + (lane & 15)]).after;
+#pragma unroll
+        for (int i = 0; i < kNF; ++i) acc[i][j] *= after;
+      }
 #pragma unroll
       for (int i = 0; i < kNF; i += GATED ? 2 : 1) {
         if constexpr (MODE == kFwd) {
@@ -396,10 +421,19 @@ struct Gemm {
       load_lds4(t.pb + (in ? n - (GATED ? t.n0 / 2 : t.n0) + 1 : 1) * (int64_t)t.ldb - 4, to + BM + wave * 64);
     }
   }
-  __device__ static __forceinline__ void scaled(const float* scales, int wm, int wn, int lane, const Acc<DT> (*acc)[kMF], v4f (*z)[kMF]) {
+  // The sums scaled; second parts of large scales are taken too or, kLate, left to the general epilogue, a row at a time
+  // (true: there are some). All of a gated bf16 tile at once put 46 registers into scratch, the experts' 8 x 32768 rows,
+  // 512 -> 512 gated, 236 to 262 us, and a branch for it in the bare epilogue took 245; fp32 has no registers left there.
+  static constexpr bool kLate = GATED && DT == kI8ToBf16;
+  __device__ static __forceinline__ bool scaled(const float* scales, int wm, int wn, int lane, const Acc<DT> (*acc)[kMF], v4f (*z)[kMF]) {
     float sx[kMF];
+    bool large = false;
 #pragma unroll
-    for (int j = 0; j < kMF; ++j) sx[j] = scales[wm + j * 16 + (lane & 15)];
+    for (int j = 0; j < kMF; ++j) {
+      const RowScale by(scales[wm + j * 16 + (lane & 15)]);
+      sx[j] = by.s;
+      large |= by.large;
+    }
 #pragma unroll
     for (int i = 0; i < kNF; ++i) {
       const v4f sw = *reinterpret_cast<const v4f*>(scales + BM + wn + i * 16 + (lane >> 4) * 4);
@@ -408,6 +442,15 @@ struct Gemm {
 #pragma unroll
         for (int q = 0; q < 4; ++q) z[i][j][q] = static_cast<float>(acc[i][j][q]) * sx[j] * sw[q];
     }
+    const bool any = ballot(large) != 0;
+    if (kLate || !any) return any;
+#pragma unroll
+    for (int j = 0; j < kMF; ++j) {
+      const float after = RowScale(scales[wm + j * 16 + (lane & 15)]).after;
+#pragma unroll
+      for (int i = 0; i < kNF; ++i) z[i][j] *= after;
+    }
+    return false;
   }
 
   // Row of b behind tile row j (forward): gated, 16 gate columns, then the same 16
@@ -676,8 +719,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void k_gemm(const GemmA
   }
   if constexpr (kInt8<DT>) {
     v4f z[kNF][kMF];
-    G::scaled(scales, wm, wn, lane, acc, z);
-    G::template finish<ACT>(a, at, wm, wn, lane, z);
+    const bool large = G::scaled(scales, wm, wn, lane, acc, z);
+    G::template finish<ACT>(a, at, wm, wn, lane, z, large, scales + wm);
   } else {
     G::template finish<ACT>(a, at, wm, wn, lane, acc);
   }
@@ -823,8 +866,8 @@ __global__ __launch_bounds__(512) void k_gemm_run(const GemmArgs a, int tiles) {
     // every wave is past its reads of the steps, and of the other scales: a tile's barriers lie between
     if (more) issue(then.t, scales + (flip ^ 1) * G::kScales);
     v4f z[kNF][kMF];
-    G::scaled(scales + flip * G::kScales, wm, wn, lane, acc, z);
-    G::template finish<ACT>(a, at, wm, wn, lane, z);
+    const bool large = G::scaled(scales + flip * G::kScales, wm, wn, lane, acc, z);
+    G::template finish<ACT>(a, at, wm, wn, lane, z, large, scales + flip * G::kScales + wm);
     if (!more) return;
     whole = t.m0 + 256 <= t.mEnd && (GATED ? t.n0 / 2 + 128 <= t.O : t.n0 + 256 <= t.N);
     at = then;
@@ -898,12 +941,13 @@ __global__ __launch_bounds__(512) void k_few(const GemmArgs a) {
     const int n = a.O - (c0 + p * 4);
     if (n <= 0) return;
     float y[4];
+    const RowScale by(sx);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float z[NW];
 #pragma unroll
       for (int h = 0; h < NW; ++h) {
-        z[h] = static_cast<float>(s[h][j]) * sx * sw[h][j];
+        z[h] = by(s[h][j], sw[h][j]);
         if (a.bias.p[r]) z[h] += bias[h][j];
       }
       y[j] = act_value<kOutOf<DT>, ACT>(z[0]);
