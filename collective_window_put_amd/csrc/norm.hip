@@ -5,7 +5,7 @@
 //   norm      h = round(x + residual); y = h / r * gain, r = sqrt(mean h^2 + eps)
 //   gradient  n = h / r, g = dout * gain: dh = dsum + (g - n mean(g n)) / r;
 //             dgain = sum over rows of dout n
-//   8 bits    m = max |x|: scale = m / 127, value = rint(x * (127 / m))
+//   8 bits    m = max |x|: scale = m / 127, value = rint(x * (127 / m)); 127 scales are a number
 //
 // All are bound by memory: a row is read once, held in registers between its
 // reductions and its outputs, and everything that is made of it is written in
@@ -23,6 +23,7 @@ namespace {
 typedef v4u v4u_any __attribute__((aligned(2)));  // at any element's alignment
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr uint32_t kLeastBits = 0x04000000u;  // 2^-119: 1/127 of less would be subnormal
+constexpr float kMostScale = 0x1.020406p121f;  // 127 times the next is infinite, and the largest number's 1/127 rounds to that
 
 struct RowArgs {
   WinTab x, residual, gain, sum, out, q8;
@@ -84,7 +85,7 @@ struct To8 {
 __device__ inline To8 to_8(uint32_t m) {
   if (m >= kInfBits) return {0.0f, __uint_as_float(0x7FC00000u), true};
   if (m < kLeastBits) return {0.0f, 0.0f, true};
-  return {127.0f / __uint_as_float(m), __uint_as_float(m) / 127.0f, false};
+  return {127.0f / __uint_as_float(m), fminf(__uint_as_float(m) / 127.0f, kMostScale), false};
 }
 // Four values as bytes: added to 1.5 * 2^23 a product is rounded to a whole
 // number, to nearest even and once, whose low byte is the sum's.

@@ -727,7 +727,8 @@ vrResult_t vr_moe_layer(vrComm_t comm, const vrMoeShape* shape, vrSlice x, const
  * together. Slices of q8 rows start at a multiple of 4 bytes (of 16: fastest).
  * A row becomes one like this: m its largest magnitude, scale = m / 127, value =
  * x * (127 / m) rounded to nearest even, each off by at most half a scale (and the
- * binary32 roundings of the two quotients and the product). A row with m below
+ * binary32 roundings of the two quotients and the product; the largest number's
+ * scale is rounded down, so that 127 scales are a number). A row with m below
  * 2^-119 (its scale would be subnormal) gets scale 0 and zeros. A row with a NaN
  * or an infinity gets scale NaN and zeros, so that everything computed from it is
  * NaN, and sets VR_ASYNC_BAD_VALUE. */

@@ -151,14 +151,16 @@ def norm_backward(dout, h, gain, eps: float, dsum=None):
 
 def to_8_bits(x):
     """(int8 values, binary32 scales) of rows of binary32 values, bit for bit: scale m / 127 and the multiplier 127 / m
-    rounded to binary32, the product rounded once; zeros below 2^-119, scale NaN where a value is no number."""
+    rounded to binary32, the product rounded once; zeros below 2^-119, scale NaN where a value is no number. The largest
+    number's scale is rounded down: 127 times it is a number."""
     x = np.asarray(x, np.float32)
     m = np.abs(x).max(-1, keepdims=True)
     bad = ~np.isfinite(x).all(-1, keepdims=True)
     none = bad | (m < np.float32(2.0 ** -119))
     m1 = np.where(none, np.float32(1), m).astype(np.float32)
+    most = np.nextafter(np.finfo(np.float32).max / np.float32(127), np.float32(0))
     value = np.rint(np.where(none, 0, x).astype(np.float64) * (np.float32(127) / m1).astype(np.float64))
-    scale = np.where(bad, np.float32(np.nan), np.where(none, np.float32(0), m1 / np.float32(127)))
+    scale = np.where(bad, np.float32(np.nan), np.where(none, np.float32(0), np.minimum(m1 / np.float32(127), most)))
     return value.astype(np.int8), scale[..., 0].astype(np.float32)
 
 
