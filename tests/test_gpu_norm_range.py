@@ -56,3 +56,41 @@ def test_a_root_whose_square_passes_binary32(cols, dtype):
         tol = (np.abs(dout[0]) * n).sum(0) * (13 * STEP + rel) + np.abs(wg) * half + TINY
         check(dg_read()[0], wg, tol, "dgain")
         job.assert_no_async_error()
+
+
+@pytest.mark.parametrize("cols", [5, 300, 3000, 9000, 40000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_that_hold_the_largest_numbers(cols, dtype):
+    # as masks have them: the lowest number in a part of a row, in all of it, beside the highest, in the residual alone
+    say(f"norm: rows of the largest numbers, cols={cols} {dtype}")
+    rng = np.random.default_rng(cols)
+    top = float(np.finfo(np.float32).max) if dtype == "f32" else float.fromhex("0x1.fep127")
+    x, res = round_to(rng.normal(size=(1, 4, cols)), dtype), np.zeros((1, 4, cols))
+    x[0, 0, cols // 2:] = -top
+    x[0, 1] = -top
+    x[0, 2, ::2], x[0, 2, 1::2] = top, -top
+    res[0, 3, 0], x[0, 3, 0] = -top, 0.0
+    h = x + res
+    g, dout = round_to(rng.normal(size=(1, cols)), dtype), round_to(rng.normal(size=(1, 4, cols)), dtype)
+    eps = float(np.float32(1e-5))
+    shape = vr.vrNormShape(DT[dtype], 4, cols, eps)
+    rel, half = root_off(cols, dtype), HALF[dtype]
+    with Job(1) as job:
+        tn = Tensors(job, dtype)
+        out, read = tn.put(shape=(4, cols))
+        total, total_read = tn.put(shape=(4, cols))
+        gs = tn.put(g)[0]
+        vr.vr_norm(job.comm, shape, tn.put(x)[0], gain=gs, residual=tn.put(res)[0], sum=total, out=out)
+        assert np.array_equal(total_read(), h)
+        want = L.norm(h[0], g[0], eps)
+        check(read()[0], want, np.abs(want) * (rel + 4 * STEP + half) + TINY, "out")
+        dh, dh_read = tn.put(shape=(4, cols))
+        dg, dg_read = tn.put(shape=(cols,))
+        need = vr.vr_norm_backward_workspace_bytes(1, shape)
+        vr.vr_norm_backward(job.comm, shape, tn.put(dout)[0], total, gain=gs, dh=dh, dgain=dg, workspace=workspace(need),
+                            workspace_bytes=need)
+        wh, wg = L.norm_backward(dout[0], h[0], g[0], eps)
+        check(dh_read()[0], wh, TINY, "dh")  # a gradient over 2^127: nothing that is left of it is a normal number
+        n = np.abs(L.norm(h[0], None, eps))
+        check(dg_read()[0], wg, (np.abs(dout[0]) * n).sum(0) * (12 * STEP + rel) + np.abs(wg) * half + TINY, "dgain")
+        job.assert_no_async_error()
