@@ -226,9 +226,10 @@ __device__ inline float down(uint32_t m, bool* bad) {
 }
 // A gradient's row is taken again where the root's square is no binary32 number, or
 // the mean of g n is so large that its product with an n (2^10 at most, the root of
-// the most columns) might not be one: h is then brought below 2 and g below 2^65, where
-// they are not, by powers of two. Sums of 2^20 products of those stay inside binary32.
-constexpr float kMostMean = 0x1p117f;
+// the most columns) could take the largest g past binary32, by half a step of 2^104: h
+// is then brought below 2 and g below 2^65, where they are not, by powers of two. Sums
+// of 2^20 products of those stay inside binary32.
+constexpr float kMostMean = 0x1p93f;
 __device__ inline bool again_scaled(float square, float mean) { return !(square < INFINITY && fabsf(mean) < kMostMean); }
 struct Scales {
   float h, g, back;  // back = h / g, what brings the scaled row's gradient back

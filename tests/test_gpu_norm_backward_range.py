@@ -121,3 +121,26 @@ def test_a_dout_that_is_no_number_stays_in_its_row_and_column(cols, dtype, size)
         want, mag = (dout[0, :, others] * n[:, others].T).sum(1), (np.abs(dout[0, :, others]) * np.abs(n[:, others].T)).sum(1)
         check(gain[others], want, mag * (11 * STEP + rel) + np.abs(want) * HALF[dtype] + TINY, "dgain")
         job.assert_no_async_error()
+
+
+@pytest.mark.parametrize("cols", [8, 520, 4100, 20000])
+def test_the_largest_g_beside_a_mean_of_the_other_sign(cols):
+    # g_0 - n_0 mean passes binary32 by a step, where the gradient, over the root, does not
+    say(f"norm gradients: the largest g, cols={cols}")
+    h = np.full((1, 1, cols), 2.0)
+    h[0, 0, 0] = 0.25
+    n = h[0, 0] / np.sqrt((h[0, 0] ** 2).mean())
+    dout = np.empty((1, 1, cols))
+    dout[0, 0, 0] = float(np.finfo(np.float32).max)
+    dout[0, 0, 1:] = (-2.0 ** 114 * cols - dout[0, 0, 0] * n[0]) / n[1:].sum()
+    dout = round_to(dout, "f32")
+    shape = vr.vrNormShape(DT["f32"], 1, cols, 1e-5)
+    with Job(1) as job:
+        tn = Tensors(job, "f32")
+        need = vr.vr_norm_backward_workspace_bytes(1, shape)
+        dh, dh_read = tn.put(shape=(1, cols), fill=5.0)
+        dg, dg_read = tn.put(shape=(cols,), fill=5.0)
+        vr.vr_norm_backward(job.comm, shape, tn.put(dout)[0], tn.put(h)[0], dh=dh, dgain=dg, workspace=workspace(need),
+                            workspace_bytes=need)
+        _back_check(dh_read()[0], dg_read()[0], dout[0], h[0], None, float(np.float32(1e-5)), None, "f32", f"cols={cols}")
+        job.assert_no_async_error()
