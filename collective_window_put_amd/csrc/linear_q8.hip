@@ -5,9 +5,9 @@
 // The sums are 32-bit integers, exact; they become binary32 once, at the end. The
 // tiles and the kernels for few rows are those of vr_linear, with matrix
 // instructions of twice the rate and half the bytes of bf16; large calls take
-// k_gemm_run. 8192 x 4096 x 4096 with gelu, bias and residual: 149 us, 1.84 POP/s
-// (bf16: 303 us); 8 x 32768 rows (15/16 used) by 32 experts,
-// 512 -> 512 gated: 244 us, 1.06 POP/s.
+// k_gemm_run. 8192 x 4096 x 4096 with gelu, bias and residual, three sets of inputs
+// in turn: 151 us, 1.82 POP/s (bf16 in the same run: 257 us); 8 x 32768 rows (15/16
+// used) by 32 experts, 512 -> 512 gated: 247 us, 1.05 POP/s.
 #include <hip/hip_runtime.h>
 
 #include "vr_gemm.hpp"

@@ -248,7 +248,10 @@ constexpr int threads_of(int tpr) { return tpr == 64 ? 256 : tpr; }
 // without a barrier and takes up to 4 pieces of it; longer rows take as many
 // threads as that needs. 8 x 4096 rows of 2048 bf16 with residual, sum and rows in
 // 8 bits: 78 us, 6.0 TB/s; 4 x 8192 rows of 512 to 8 bits by group counts: 11 us; one
-// row of 4096: 2.9 us, a launch.
+// row of 4096: 2.9 us, a launch. fp32: 8 x 2048 rows of 4096 with residual, sum and
+// out 153 us, 7.0 TB/s. Four bf16 pieces to each of 1024 threads are too many: 33
+// registers of them, the gain's in the main, lie in scratch, and 4096 rows of 12288
+// take 270 us, 1.5 TB/s (to 8 bits, without gain or residual, 36).
 template <int DT, int TPR, int P, bool NORM, int MODE>
 __global__ __launch_bounds__(threads_of(TPR)) void k_rows(const RowArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = threads_of(TPR) / TPR, kW = TPR / 64;
@@ -507,7 +510,7 @@ struct BackArgs {
 // the sums of a whole rank would be atomics, whose order changes results, and one
 // row of sums per row another pass over the data. Three rows are read for one that
 // is written: 8 x 2048 rows of 4096 bf16 with dsum and dgain 98 us, 5.5 TB/s (other
-// threads to a row and 512 to 2048 slots: 98 to 104).
+// threads to a row and 512 to 2048 slots: 98 to 104); fp32 5.0 to 5.6 TB/s.
 // The least waves to a SIMD that its registers have to leave room for: 64 of them let two workgroups of 16 waves onto a
 // compute unit, which the compiler misses by five (2000 rows of 4096 fp32: 25.4 us, else 27.4); the other modes would spill.
 template <int DT, int TPR, int P, int MODE> constexpr int kBackWaves = DT == VR_DT_F32 && TPR == 1024 && P == 1 && MODE == kWhole ? 8 : 1;
@@ -643,7 +646,8 @@ __global__ __launch_bounds__(threads_of(TPR), (kBackWaves<DT, TPR, P, MODE>)) vo
 }
 
 // Rows too long for registers (and those of less than a piece): dh, and the
-// roots for the sums of dgain.
+// roots for the sums of dgain. h and dout are read twice here and once more for
+// dgain: 2048 rows of 32768 bf16 with dsum 287 us, 1.9 TB/s of what is needed once.
 template <int DT>
 __global__ __launch_bounds__(kLongThreads) void k_norm_back_long(const BackArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, T = kLongThreads;

@@ -753,7 +753,7 @@ typedef struct {
  *   may be residual's own slice), out [rows][cols] = y, q8 [rows] = y as q8 rows
  *   (from y unrounded)
  * Statistics are binary32 and do not overflow: a row of finite h has a finite
- * root. No other ranges may overlap an output (VR_ERR_INVALID_ARGUMENT). */
+ * root, with any eps. No other ranges may overlap an output (VR_ERR_INVALID_ARGUMENT). */
 vrResult_t vr_norm(vrComm_t comm, const vrNormShape* shape, vrSlice x, vrSlice residual, vrSlice gain,
                    vrSlice sum, vrSlice out, vrSlice q8, void* stream);
 
@@ -764,9 +764,9 @@ vrResult_t vr_norm(vrComm_t comm, const vrNormShape* shape, vrSlice x, vrSlice r
  *   n = h / r, g = dout * gain: the gradient of x and of residual alike; may be
  *   dsum's own slice
  *   dgain [cols] = sum over the rank's rows of dout * n (zeros without rows)
- * At least one of the two is wanted. Sums run in a fixed order. Squares and
- * products that pass binary32 are taken again, scaled: where h and g are finite,
- * dh is as the formula has it. */
+ * At least one of the two is wanted; the workspace is needed with either. Sums
+ * run in a fixed order. Squares and products that pass binary32 are taken again,
+ * scaled: where h and dout * gain are finite, dh is as the formula has it. */
 size_t vr_norm_backward_workspace_bytes(int nranks, const vrNormShape* shape);
 vrResult_t vr_norm_backward(vrComm_t comm, const vrNormShape* shape, vrSlice dout, vrSlice h, vrSlice gain,
                             vrSlice dsum, vrSlice dh, vrSlice dgain, void* workspace, size_t workspace_bytes,
@@ -786,7 +786,9 @@ vrResult_t vr_dequantize(vrComm_t comm, vrSlice q8, int dtype, int rows, int col
  *   x [rows] q8 rows of `in` values: a scale for each token
  *   w [groups][N] q8 rows of `in` values: a scale for each channel
  *   bias, residual, group_rows, out: as vr_linear
- * Products of values are summed in 32-bit integers, exactly for any bytes. */
+ * Products of values are summed in 32-bit integers, exactly for any bytes; a sum
+ * becomes binary32 and is multiplied by x's scale and by w's, where only the result
+ * has to be a binary32 number. */
 vrResult_t vr_linear_q8(vrComm_t comm, const vrLinearShape* shape, vrSlice x, vrSlice w, vrSlice bias,
                         vrSlice residual, const int32_t* group_rows, vrSlice out, void* stream);
 
