@@ -505,15 +505,18 @@ struct BackArgs {
   float eps;
 };
 
+// The least waves to a SIMD that a gradient's registers have to leave room for: 64 registers let two workgroups of 16 waves
+// onto a compute unit, which the compiler misses by five (2000 rows of 4096 fp32: 25.4 us, else 27.4); the other modes
+// would spill.
+template <int DT, int TPR, int P, int MODE>
+constexpr int kBackWaves = DT == VR_DT_F32 && TPR == 1024 && P == 1 && MODE == kWhole ? 8 : 1;
+
 // A row to TPR threads as above. Workgroup x takes rows x, x + slots, ... (of
 // one wave: four at a time) and keeps its columns' sums for dgain in registers:
 // the sums of a whole rank would be atomics, whose order changes results, and one
 // row of sums per row another pass over the data. Three rows are read for one that
 // is written: 8 x 2048 rows of 4096 bf16 with dsum and dgain 98 us, 5.5 TB/s (other
 // threads to a row and 512 to 2048 slots: 98 to 104); fp32 5.0 to 5.6 TB/s.
-// The least waves to a SIMD that its registers have to leave room for: 64 of them let two workgroups of 16 waves onto a
-// compute unit, which the compiler misses by five (2000 rows of 4096 fp32: 25.4 us, else 27.4); the other modes would spill.
-template <int DT, int TPR, int P, int MODE> constexpr int kBackWaves = DT == VR_DT_F32 && TPR == 1024 && P == 1 && MODE == kWhole ? 8 : 1;
 template <int DT, int TPR, int P, int MODE>
 __global__ __launch_bounds__(threads_of(TPR), (kBackWaves<DT, TPR, P, MODE>)) void k_norm_back(const BackArgs a) {
   constexpr int kC = Elem<DT>::kChunk, kES = Elem<DT>::kSize, kRows = threads_of(TPR) / TPR, kW = TPR / 64;

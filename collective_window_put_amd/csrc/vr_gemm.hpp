@@ -181,7 +181,8 @@ struct RowScale {
 // elements 271 to 257.
 template <int DT, int ACT, bool GATED, int NF, int MF, bool PAIRS, bool BARE>
 __device__ inline void epilogue_whole(const GemmArgs& a, int r, int g, int row0, int m0, int mEnd, int c0, int lane,
-                                      v4f (*acc)[MF], [[maybe_unused]] bool large, [[maybe_unused]] const float* row_scales) {
+                                      v4f (*acc)[MF], [[maybe_unused]] bool large,
+                                      [[maybe_unused]] const float* row_scales) {
   constexpr int kES = Elem<DT>::kSize, NO = GATED ? NF / 2 : NF, S = GATED ? 2 : 1;
   const int m1 = m0 + (lane & 15), col = c0 + (lane >> 4) * (PAIRS ? 8 : 4);
   const auto off = [](int i) { return PAIRS ? (i >> 1) * 32 + (i & 1) * 4 : i * 16; };
@@ -373,9 +374,11 @@ struct Gemm {
       if (GATED ? t.n0 / 2 + BN / 2 <= a.O : t.n0 + BN <= a.N) {
         const int c0 = GATED ? (t.n0 + wn) / 2 : t.n0 + wn;
         if (a.bias.p[s.r] || a.residual.p[s.r] || a.preact.p[s.r] || large)
-          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, false>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc, large, row_scales);
+          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, false>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc,
+                                                                          large, row_scales);
         else
-          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, true>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc, large, row_scales);
+          epilogue_whole<kOutOf<DT>, ACT, GATED, kNF, kMF, kPairs, true>(a, s.r, s.g, s.row0, t.m0 + wm, t.mEnd, c0, lane, acc,
+                                                                          large, row_scales);
         return;
       }
     }
