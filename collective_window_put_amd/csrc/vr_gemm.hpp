@@ -796,8 +796,9 @@ struct GroupTable {
 // gelu, bias, residual, 149 us) the matrix units are 42 % busy and the card's
 // power matters: zeros take 112 us where random values take 131.
 //
-// fp32 results keep 27 to 38 registers in scratch and read them back behind the next
-// tile's loads: 231 us dense and 338 by expert, bf16 ones 152 and 247.
+// fp32 results are slower than their bytes: without a gate 27 to 37 registers lie in
+// scratch and are read back behind the next tile's loads (the dense case 231 us, bf16
+// 152), gated 3 at most (the experts 338 and 247, of which 250 MB more take about 40).
 //
 // Tiles are dealt out by the buffers' capacity, as the used rows are known on the
 // device alone: where a rank's buffer is only partly used, so are the XCDs. The same
